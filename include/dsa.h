@@ -74,7 +74,10 @@ enum dsa_op {
     DSA_OP_TOPK = 2,
     DSA_OP_SPARSE_ATTN = 3,
     DSA_OP_FORWARD = 4,
-    DSA_OP_FORWARD_HOST = 5
+    DSA_OP_FORWARD_HOST = 5,
+    DSA_OP_NORM_ROPE_BWD = 6, /* k = norm_dim */
+    DSA_OP_PAGED_SELECT = 7,  /* k = top-k size; ia */
+    DSA_OP_PAGED_ATTN = 8     /* k = k_sel (0: dense); aa */
 };
 
 /* Query rows per chunk of dsa_forward_host (the pipeline's fill and drain
@@ -141,7 +144,8 @@ DSA_API const char* dsa_status_string(int status);
 
 /* Library ABI version (major*1000 + minor).  1001: dsa_indexer_args gained
  * k_per_row.  1002: dsa_sparse_attn_bwd.  1003: dsa_attn_target,
- * dsa_indexer_kl. */
+ * dsa_indexer_kl.  1004: dsa_norm_rope, dsa_norm_rope_bwd and the paged cache
+ * (dsa_cache_append, dsa_paged_scores, dsa_paged_select, dsa_paged_attn). */
 DSA_API int dsa_version(void);
 
 /* Workspace bytes needed by `op` for this problem (k = top-k size, used by
@@ -337,6 +341,153 @@ DSA_API int dsa_forward(const dsa_seqs* seqs, const dsa_indexer_args* ia, const 
 DSA_API int dsa_forward_host(const dsa_seqs* seqs, const dsa_indexer_args* ia, const dsa_attn_args* aa, int32_t k,
                              int32_t* idx_out, int64_t ld_idx, void* ws, size_t ws_bytes, dsa_stream_t stream,
                              dsa_stream_t h2d_stream, dsa_stream_t d2h_stream);
+
+/* ---------------------------------------------------------------------------
+ * Queries and keys: norm and position rotation
+ *
+ * A per-row transform, applied in this order to a row x of `dim` columns:
+ * - RMS norm of the columns [0, norm_dim) (none when norm_dim is 0):
+ *   u_c = x_c * r * weight_c, r = 1 / sqrt(mean(x_c^2, c < norm_dim) + eps);
+ *   weight NULL: all ones.
+ * - Rotation of the columns [rope_begin, rope_begin + rope_dim) (none when
+ *   rope_dim is 0) by the angles of the row's position: pair i of them is
+ *   (2i, 2i + 1) when rope_interleaved, else (i, i + rope_dim / 2), counted from
+ *   rope_begin, and (a, b) becomes (a cos_i - b sin_i, b cos_i + a sin_i).
+ *   cos_sin [rope_positions, rope_dim] holds the cosines of a position's
+ *   rope_dim / 2 angles, then their sines.
+ * Other columns pass unchanged.  In the MLA layout the shared KV row is
+ * norm_dim 512, rope columns [512, 576); a query head's row has the same rope
+ * columns and no norm; a per-head norm of queries and keys is norm_dim = dim.
+ * Arithmetic is fp32 (the indexer key of dsa_cache_append: 64 bits), with one
+ * rounding at the end.  Aligned rows (16-byte aligned pointers and strides,
+ * dim, norm_dim, rope_begin and rope_dim multiples of 8, half-split rope_dim of
+ * 16) are moved in 16-byte pieces; any other rows take a scalar path with the
+ * same results up to the order of sums.  dim <= 2048.                        */
+typedef struct dsa_row_args {
+    int32_t norm_dim;
+    float eps;
+    const float* weight;      /* nullable, [norm_dim] */
+    int32_t rope_begin, rope_dim;
+    int32_t rope_interleaved;
+    const float* cos_sin;     /* [rope_positions, rope_dim] */
+    int64_t rope_positions;
+} dsa_row_args;
+
+/* y[t, h, :] = the transform of x[t, h, :] at token t's position (seqs rule),
+ * for heads rows a token (heads = 1 for the shared KV row).  dtype (x and y):
+ * DSA_BF16 or DSA_F32.  y may be x (same strides).  ra NULL: a copy.  A token
+ * whose position is invalid or >= rope_positions is recorded as DSA_ERR_INDEX
+ * and its rows are left as they were.  Workspace: a status header. */
+DSA_API int dsa_norm_rope(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtype, int32_t heads, int32_t dim,
+                          const void* x, int64_t x_stride_tok, int64_t x_stride_head, void* y, int64_t y_stride_tok,
+                          int64_t y_stride_head, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Backward of dsa_norm_rope: d_x (of x's dtype) and d_weight (float
+ * [norm_dim], summed over all rows; nullable) are written from x and the output
+ * gradient d_y (same dtype).  With g the transposed rotation of d_y,
+ * x^ = x r and n = norm_dim:
+ *     d_x_c = r (g_c w_c - x^_c mean_n(g w x^))  (c < n),   g_c elsewhere
+ *     d_weight_c = sum over rows of g_c x^_c
+ * d_weight is summed in a fixed order: the same call gives the same bits.  x is
+ * not read (may be NULL) when norm_dim is 0.  d_x may be neither x nor d_y.
+ * Rows of an invalid token: as above, and they add nothing to d_weight.
+ * Workspace: DSA_OP_NORM_ROPE_BWD with k = norm_dim. */
+DSA_API int dsa_norm_rope_bwd(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtype, int32_t heads, int32_t dim,
+                              const void* x, int64_t x_stride_tok, int64_t x_stride_head, const void* d_y,
+                              int64_t d_y_stride_tok, int64_t d_y_stride_head, void* d_x, int64_t d_x_stride_tok,
+                              int64_t d_x_stride_head, float* d_weight, void* ws, size_t ws_bytes,
+                              dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged cache
+ *
+ * Position s of sequence b lives in row s % page_size of page
+ * table[b * ld_table + s / page_size] of every pool.  A pool is num_pages pages,
+ * *_page_stride elements apart: KV rows (row stride given with the pool's
+ * pointer), indexer-key rows of 128 (contiguous), one fp32 scale per indexer key
+ * (contiguous).  page_size is any size from 1 to 65536; sequences may share
+ * pages that they only read.  seqs describes the lengths AFTER the new tokens:
+ * cu_seqlens_k are prefix sums of the sequences' cached lengths (total_k their
+ * sum) and no pool is indexed by them.  Table entries past a sequence's last
+ * page are not read.  A position whose entry is not in [0, num_pages) is
+ * recorded as DSA_ERR_INDEX and touches no memory.                           */
+typedef struct dsa_pages {
+    int32_t page_size;
+    int64_t num_pages;
+    const int32_t* table;      /* device, [batch, ld_table] */
+    int64_t ld_table;          /* >= ceil(max_seqlen_k / page_size) */
+    int64_t kv_page_stride;    /* elements between pages of the KV (or K) pool */
+    int64_t v_page_stride;     /* of a separate V pool */
+    int64_t idx_page_stride;   /* of the indexer-key pool */
+    int64_t scale_page_stride; /* of the indexer-key scale pool */
+} dsa_pages;
+
+/* Rows to append (dsa_cache_append).  Either part may be absent (NULL kv_new or
+ * idx_new).  dtype (kv_new, kv, idx_new): DSA_BF16 or DSA_F32.  idx_dtype: the
+ * indexer-key pool's, DSA_E4M3 (codes, with idx_scale) or DSA_F32 (idx_scale
+ * NULL).  kv_row / idx_row: transforms, NULL for none.  A pool of V rows apart
+ * from K is a second call with its own kv, kv_stride and kv_page_stride. */
+typedef struct dsa_append_args {
+    int32_t dtype, dim;         /* dim: columns of a KV row */
+    const void* kv_new;         /* [total_q, >= dim] */
+    int64_t kv_new_stride;
+    void* kv;                   /* KV pool */
+    int64_t kv_stride;
+    const dsa_row_args* kv_row;
+    int32_t idx_dtype;
+    const void* idx_new;        /* [total_q, >= 128] */
+    int64_t idx_new_stride;
+    void* idx;                  /* indexer-key pool (16-byte aligned, as its page stride) */
+    float* idx_scale;
+    const dsa_row_args* idx_row;
+} dsa_append_args;
+
+/* Append the queries' tokens to the cache: token i of sequence b goes to
+ * position seqlen_k(b) - seqlen_q(b) + i.  The KV row is kv_row's transform of
+ * kv_new, rounded to the pool's type.  The indexer key is idx_row's transform of
+ * idx_new in 64 bits; FP8: scale = fp32(amax / 448) (1 when that is 0), codes =
+ * the e4m3 values nearest to key / scale (ties to even, saturating).  All other
+ * rows of the pools keep their contents.  Two tokens of one call must not map to
+ * the same row.  Workspace: a status header. */
+DSA_API int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_append_args* ap, void* ws,
+                             size_t ws_bytes, dsa_stream_t stream);
+
+/* Indexer scores (as dsa_index_scores) of the folded queries u, s_row (from
+ * dsa_fold) over the paged indexer keys k_idx / k_idx_scale (dtype DSA_E4M3, or
+ * DSA_F32 with NULL scales), for query rows [row_begin, row_begin + row_count):
+ * scores float [row_count, ld_scores], ReLU(s_row * s_k[s] * (u . k_s)) for
+ * s <= pos, -inf for pos < s < ld_scores and for positions without a valid
+ * page.  dsa_topk takes these scores.  Workspace: a status header. */
+DSA_API int dsa_paged_scores(const dsa_seqs* seqs, const dsa_pages* pages, int32_t dtype, const void* u,
+                             const float* s_row, const void* k_idx, const float* k_idx_scale, int64_t row_begin,
+                             int64_t row_count, float* scores, int64_t ld_scores, void* ws, size_t ws_bytes,
+                             dsa_stream_t stream);
+
+/* dsa_select over the paged indexer keys: ia->k_idx and ia->k_idx_scale are
+ * the pools.  The scores pass through the workspace (DSA_OP_PAGED_SELECT), at
+ * most 1 GiB of them at a time (or one row's, where that is more). */
+DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_indexer_args* ia, int32_t k,
+                             int32_t* idx, int64_t ld_idx, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Attention of the queries over the paged KV rows.  aa as for dsa_sparse_attn,
+ * with aa->k (and aa->v) the pools and k_stride the row stride inside a page.
+ * idx NULL (k_sel 0): dense causal, keys 0..pos.  Else query t attends to the
+ * valid slots j < k_sel of idx row t (local positions, as dsa_paged_select
+ * leaves them; -1 unused).  A row with nothing to attend to gives out = 0 and
+ * lse = -inf.  Slots with an index >= seqlen_k(b) or without a valid page are
+ * skipped and recorded; so are, in the fp32 dense form, positions without a
+ * valid page (in the bf16 dense form such a position counts as a row of zeros).
+ * A token whose position is invalid is recorded, and its rows (where tokens are
+ * handled together, theirs too) are left as they were.
+ * Supported: DSA_BF16 with heads <= 128, dk = 576, dv = 512, v = k (V the
+ * leading columns), alignment as for dsa_sparse_attn (kv_page_stride a multiple
+ * of 8 too), k_sel <= 2048; DSA_F32 with heads <= 32 and dk, dv in {32, 64, 96,
+ * 128}, V its own pool or k's.  scale >= 0.
+ * With fewer than 128 heads the bf16 dense form handles 128 / heads tokens of
+ * a sequence together; a masked key among those tokens' own rows then has weight
+ * 0 but must be finite.  Workspace: DSA_OP_PAGED_ATTN with k = k_sel. */
+DSA_API int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_args* aa, const int32_t* idx,
+                           int64_t ld_idx, int32_t k_sel, void* ws, size_t ws_bytes, dsa_stream_t stream);
 
 /* Synchronise `stream`, return the first device-side error recorded in the
  * workspace status header since the last call (DSA_OK if none), write its

@@ -438,6 +438,192 @@ int run_attn(const dsa_seqs* s, const dsa_attn_args* aa, const int32_t* idx, int
     return cuda_status();
 }
 
+// ---------------------------------------------------------------------------
+// Row transforms and the paged cache
+// ---------------------------------------------------------------------------
+RowXform row_xform(const dsa_row_args* ra) {
+    RowXform x;
+    memset(&x, 0, sizeof(x));
+    x.interleaved = 1;
+    if (!ra) return x;
+    x.norm_dim = ra->norm_dim;
+    x.eps = ra->eps;
+    x.weight = ra->norm_dim ? ra->weight : nullptr;
+    x.rope_begin = ra->rope_dim ? ra->rope_begin : 0;
+    x.rope_dim = ra->rope_dim;
+    x.interleaved = ra->rope_dim ? ra->rope_interleaved != 0 : 1;
+    x.cos_sin = ra->rope_dim ? ra->cos_sin : nullptr;
+    x.rope_positions = ra->rope_positions;
+    return x;
+}
+
+int check_row(const dsa_row_args* ra, int32_t dim) {
+    if (dim < 1) return DSA_ERR_INVALID_ARG;
+    if (dim > kRowMaxDim) return DSA_ERR_UNSUPPORTED;
+    if (!ra) return DSA_OK;
+    if (ra->norm_dim < 0 || ra->norm_dim > dim || ra->rope_dim < 0 || ra->rope_dim % 2) return DSA_ERR_INVALID_ARG;
+    if (ra->norm_dim && (!(ra->eps >= 0.f) || !aligned(ra->weight, 4))) return DSA_ERR_INVALID_ARG;
+    if (ra->rope_dim && (ra->rope_begin < 0 || ra->rope_begin > dim - ra->rope_dim || !ra->cos_sin || !aligned(ra->cos_sin, 4) ||
+                         ra->rope_positions < 0))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+size_t norm_rope_bwd_ws(int32_t norm_dim) {
+    return align256(kHdr + (size_t)kNormRopeBwdBlocks * (size_t)norm_dim * 4);
+}
+
+int check_rows(int64_t tokens, int32_t heads, int32_t dim, int32_t dtype, const void* p, int64_t stride_tok,
+               int64_t stride_head) {
+    if ((tokens && !p) || !aligned(p, dtype == DSA_BF16 ? 2 : 4)) return DSA_ERR_INVALID_ARG;
+    if (stride_head < dim || stride_tok < (int64_t)(heads - 1) * stride_head + dim) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+constexpr int32_t kMaxPageSize = 65536;
+
+int check_pages(const dsa_seqs* s, const dsa_pages* pg) {
+    if (!pg || pg->page_size < 1 || pg->num_pages < 0) return DSA_ERR_INVALID_ARG;
+    if (pg->page_size > kMaxPageSize || pg->num_pages > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    if (pg->ld_table < (s->max_seqlen_k + pg->page_size - 1) / pg->page_size) return DSA_ERR_INVALID_ARG;
+    if (s->max_seqlen_k && !pg->table) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// a pool's pages: rows `row_stride` elements apart, `width` of them used
+bool pool_ok(const dsa_pages* pg, int64_t page_stride, int64_t row_stride, int64_t width) {
+    return row_stride >= width && page_stride >= (pg->page_size - 1) * row_stride + width;
+}
+
+PageView page_view(const dsa_pages* pg) {
+    PageView v;
+    v.table = pg->table;
+    v.ld_table = pg->ld_table;
+    v.num_pages = pg->num_pages;
+    v.page_size = pg->page_size;
+    v.shift = -1;
+    for (int i = 0; i <= 16; ++i)
+        if (pg->page_size == (1 << i)) v.shift = i;
+    return v;
+}
+
+// dsa_paged_select: folded queries, then the scores of `rows` queries at a time.
+struct PagedSelectLayout {
+    size_t u, s_row, scores, total;
+    int64_t rows;
+};
+
+PagedSelectLayout paged_select_layout(const dsa_seqs* s, const dsa_indexer_args* ia) {
+    PagedSelectLayout L;
+    const WsLayout W = ws_layout(s, ia, 0, false, false);
+    L.u = W.u;
+    L.s_row = W.s_row;
+    L.scores = W.total;
+    const size_t row = (size_t)s->max_seqlen_k * 4;
+    L.rows = row ? (int64_t)(((size_t)1 << 30) / row) : s->total_q;
+    if (L.rows > 128) L.rows &= ~(int64_t)127;  // whole blocks of query rows
+    if (L.rows < 1) L.rows = 1;
+    if (L.rows > s->total_q) L.rows = s->total_q;
+    L.total = align256(L.scores + (size_t)L.rows * row);
+    return L;
+}
+
+// Work items and parts of the paged attention.  Both follow from the shapes
+// alone, so the workspace size agrees with the call.
+struct PagedAttnPlan {
+    int group;
+    int64_t groups;
+    int splits;
+    size_t part_lse, part_o, total;
+};
+
+constexpr int kMaxParts = 64;
+
+PagedAttnPlan paged_attn_plan(const dsa_seqs* s, const dsa_attn_args* aa, int32_t k_sel) {
+    PagedAttnPlan p;
+    p.group = 1;
+    p.groups = s->total_q;
+    p.splits = 1;
+    const int64_t keys = k_sel > 0 ? k_sel : s->max_seqlen_k;
+    size_t rows, cols;
+    if (aa->dtype == DSA_BF16) {
+        if (k_sel == 0 && aa->heads <= 64) {
+            p.group = 128 / aa->heads;
+            if (p.group > s->max_seqlen_q) p.group = s->max_seqlen_q > 0 ? (int)s->max_seqlen_q : 1;
+            if (p.group > 1) p.groups = s->total_q / p.group + s->batch;
+        }
+        // An item's time in units of a 64-key tile: its tiles, 3 for its start and
+        // end, 2 more to write partial rows; joining them costs a launch (1.5) and
+        // their traffic.  Take the number of parts with the least.
+        const int64_t pairs = sm_count() / 2, tiles = (keys + 63) / 64;
+        double best = 0;
+        for (int64_t n = 1; n <= kMaxParts && n <= (tiles > 1 ? tiles : 1); ++n) {
+            if (n > 1 && p.groups * n > 4 * pairs) break;
+            const int64_t waves = (p.groups * n + pairs - 1) / pairs;
+            const double cost = (double)waves * (double)((tiles + n - 1) / n + 3 + (n > 1 ? 2 : 0)) +
+                                (n > 1 ? 1.5 + 0.03 * (double)(p.groups * n) : 0.0);
+            if (n == 1 || cost < best) {
+                best = cost;
+                p.splits = (int)n;
+            }
+        }
+        rows = (size_t)p.groups * p.splits * 128;
+        cols = 512;
+    } else {
+        // four blocks an SM, parts of at least 64 keys
+        const int64_t want = p.groups > 0 ? ((int64_t)sm_count() * 4 + p.groups - 1) / p.groups : 1;
+        const int64_t most = (keys + 63) / 64;
+        int64_t n = want < most ? want : most;
+        p.splits = (int)(n < 1 ? 1 : n > kMaxParts ? kMaxParts : n);
+        rows = (size_t)p.groups * p.splits * aa->heads;
+        cols = (size_t)aa->dv;
+    }
+    p.part_lse = kHdr;
+    p.part_o = p.splits > 1 ? align256(kHdr + rows * 4) : kHdr;
+    p.total = p.splits > 1 ? align256(p.part_o + rows * cols * 4) : kHdr;
+    return p;
+}
+
+int run_paged_scores(const dsa_seqs* s, const dsa_pages* pg, int32_t dtype, const void* u, const float* s_row,
+                     const void* k_idx, const float* k_scale, int64_t row_begin, int64_t row_count, float* scores,
+                     int64_t ld, bool fill, StatusHdr* h, cudaStream_t st) {
+    PagedScoresArgs a;
+    memset(&a, 0, sizeof(a));
+    a.sv = seq_view(s);
+    a.pv = page_view(pg);
+    a.max_seqlen_q = s->max_seqlen_q;
+    a.total_q = s->total_q;
+    a.u = u;
+    a.s_row = s_row;
+    a.k = k_idx;
+    a.k_page_stride = pg->idx_page_stride;
+    a.k_scale = k_scale;
+    a.scale_page_stride = pg->scale_page_stride;
+    a.row_begin = row_begin;
+    a.row_count = row_count;
+    a.scores = scores;
+    a.ld = ld;
+    a.fill = fill;
+    a.cols = fill ? ld : s->max_seqlen_k;
+    a.st = h;
+    if (!launch_paged_scores(a, dtype == DSA_E4M3, st)) return DSA_ERR_CUDA;
+    return cuda_status();
+}
+
+int check_idx_pool(const dsa_pages* pg, int32_t dtype, const void* k_idx, const float* k_scale) {
+    if (!aligned(k_idx, 16) || !pool_ok(pg, pg->idx_page_stride, 128, 128)) return DSA_ERR_INVALID_ARG;
+    if (dtype == DSA_E4M3) {
+        if (pg->num_pages && (!k_idx || !k_scale)) return DSA_ERR_INVALID_ARG;
+        if (pg->idx_page_stride % 16 || !pool_ok(pg, pg->scale_page_stride, 1, 1)) return DSA_ERR_INVALID_ARG;
+    } else if (dtype == DSA_F32) {
+        if (k_scale) return DSA_ERR_UNSUPPORTED;
+        if ((pg->num_pages && !k_idx) || pg->idx_page_stride % 4) return DSA_ERR_INVALID_ARG;
+    } else {
+        return DSA_ERR_UNSUPPORTED;
+    }
+    return DSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -455,7 +641,7 @@ const char* dsa_status_string(int status) {
     return "unknown status";
 }
 
-int dsa_version(void) { return 1003; }
+int dsa_version(void) { return 1004; }
 
 int dsa_workspace_size(int op, const dsa_seqs* seqs, int32_t k, const dsa_indexer_args* ia, const dsa_attn_args* aa,
                        size_t* bytes) {
@@ -477,6 +663,18 @@ int dsa_workspace_size(int op, const dsa_seqs* seqs, int32_t k, const dsa_indexe
         case DSA_OP_FORWARD_HOST:
             if (!ia || !aa || k < 1 || aa->heads < 1 || aa->dk < 1 || aa->dv < 1) return DSA_ERR_INVALID_ARG;
             *bytes = host_layout(seqs, ia, aa, k).total;
+            return DSA_OK;
+        case DSA_OP_NORM_ROPE_BWD:
+            if (k < 0) return DSA_ERR_INVALID_ARG;
+            *bytes = norm_rope_bwd_ws(k);
+            return DSA_OK;
+        case DSA_OP_PAGED_SELECT:
+            if (!ia || k < 1) return DSA_ERR_INVALID_ARG;
+            *bytes = paged_select_layout(seqs, ia).total;
+            return DSA_OK;
+        case DSA_OP_PAGED_ATTN:
+            if (!aa || k < 0 || aa->heads < 1 || aa->dv < 1) return DSA_ERR_INVALID_ARG;
+            *bytes = paged_attn_plan(seqs, aa, k).total;
             return DSA_OK;
     }
     return DSA_ERR_INVALID_ARG;
@@ -816,6 +1014,247 @@ int dsa_forward_host(const dsa_seqs* seqs, const dsa_indexer_args* ia, const dsa
     for (int b = 0; b < 2 && b < nchunks; ++b)
         if (cudaStreamWaitEvent(st, ev_o[b], 0) != cudaSuccess) return done(DSA_ERR_CUDA);
     return done(DSA_OK);
+}
+
+int dsa_norm_rope(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtype, int32_t heads, int32_t dim, const void* x,
+                  int64_t x_stride_tok, int64_t x_stride_head, void* y, int64_t y_stride_tok, int64_t y_stride_head,
+                  void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    const Range range("dsa_norm_rope");
+    int r = check_seqs(seqs);
+    if (!r && heads < 1) r = DSA_ERR_INVALID_ARG;
+    if (!r) r = check_row(ra, dim);
+    if (!r && dtype != DSA_BF16 && dtype != DSA_F32) r = DSA_ERR_UNSUPPORTED;
+    if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, x, x_stride_tok, x_stride_head);
+    if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, y, y_stride_tok, y_stride_head);
+    if (!r && x == y && (x_stride_tok != y_stride_tok || x_stride_head != y_stride_head)) r = DSA_ERR_INVALID_ARG;
+    if (!r) r = check_ws(ws, ws_bytes, kHdr);
+    if (r) return r;
+    NormRopeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.sv = seq_view(seqs);
+    a.total_q = seqs->total_q;
+    a.heads = heads;
+    a.dim = dim;
+    a.ra = row_xform(ra);
+    a.x = x;
+    a.x_stride_tok = x_stride_tok;
+    a.x_stride_head = x_stride_head;
+    a.y = y;
+    a.y_stride_tok = y_stride_tok;
+    a.y_stride_head = y_stride_head;
+    a.st = hdr(ws);
+    if (!launch_norm_rope(a, dtype == DSA_BF16, (cudaStream_t)stream)) return DSA_ERR_CUDA;
+    return cuda_status();
+}
+
+int dsa_norm_rope_bwd(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtype, int32_t heads, int32_t dim,
+                      const void* x, int64_t x_stride_tok, int64_t x_stride_head, const void* d_y, int64_t d_y_stride_tok,
+                      int64_t d_y_stride_head, void* d_x, int64_t d_x_stride_tok, int64_t d_x_stride_head, float* d_weight,
+                      void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    const Range range("dsa_norm_rope_bwd");
+    int r = check_seqs(seqs);
+    if (!r && heads < 1) r = DSA_ERR_INVALID_ARG;
+    if (!r) r = check_row(ra, dim);
+    if (!r && dtype != DSA_BF16 && dtype != DSA_F32) r = DSA_ERR_UNSUPPORTED;
+    const int32_t n = !r && ra ? ra->norm_dim : 0;
+    if (!r && n) r = check_rows(seqs->total_q, heads, dim, dtype, x, x_stride_tok, x_stride_head);
+    if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, d_y, d_y_stride_tok, d_y_stride_head);
+    if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, d_x, d_x_stride_tok, d_x_stride_head);
+    if (!r && seqs->total_q && (d_x == x || d_x == d_y)) r = DSA_ERR_INVALID_ARG;
+    if (!r) r = check_ws(ws, ws_bytes, norm_rope_bwd_ws(n));
+    if (r) return r;
+    NormRopeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.sv = seq_view(seqs);
+    a.total_q = seqs->total_q;
+    a.heads = heads;
+    a.dim = dim;
+    a.ra = row_xform(ra);
+    if (n) {
+        a.x = x;
+        a.x_stride_tok = x_stride_tok;
+        a.x_stride_head = x_stride_head;
+    }
+    a.dy = d_y;
+    a.dy_stride_tok = d_y_stride_tok;
+    a.dy_stride_head = d_y_stride_head;
+    a.y = d_x;
+    a.y_stride_tok = d_x_stride_tok;
+    a.y_stride_head = d_x_stride_head;
+    a.dw_part = (float*)((uint8_t*)ws + kHdr);
+    a.st = hdr(ws);
+    if (!launch_norm_rope_bwd(a, dtype == DSA_BF16, d_weight, (cudaStream_t)stream)) return DSA_ERR_CUDA;
+    return cuda_status();
+}
+
+int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_append_args* ap, void* ws, size_t ws_bytes,
+                     dsa_stream_t stream) {
+    const Range range("dsa_cache_append");
+    int r = check_seqs(seqs);
+    if (!r) r = check_pages(seqs, pages);
+    if (r) return r;
+    if (!ap || (!ap->kv_new && !ap->idx_new && seqs->total_q)) return DSA_ERR_INVALID_ARG;
+    if (ap->dtype != DSA_BF16 && ap->dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+    const int elem = ap->dtype == DSA_BF16 ? 2 : 4;
+    AppendArgs a;
+    memset(&a, 0, sizeof(a));
+    if (ap->kv_new) {
+        r = check_row(ap->kv_row, ap->dim);
+        if (r) return r;
+        if (!ap->kv || !aligned(ap->kv, elem) || !aligned(ap->kv_new, elem) || ap->kv_new_stride < ap->dim ||
+            !pool_ok(pages, pages->kv_page_stride, ap->kv_stride, ap->dim))
+            return DSA_ERR_INVALID_ARG;
+        a.dim = ap->dim;
+        a.kv_new = ap->kv_new;
+        a.kv_new_stride = ap->kv_new_stride;
+        a.kv = ap->kv;
+        a.kv_stride = ap->kv_stride;
+        a.kv_page_stride = pages->kv_page_stride;
+        a.kv_row = row_xform(ap->kv_row);
+        ++a.parts;
+    }
+    if (ap->idx_new) {
+        r = check_row(ap->idx_row, 128);
+        if (!r) r = check_idx_pool(pages, ap->idx_dtype, ap->idx, ap->idx_scale);
+        if (r) return r;
+        if (!ap->idx || !aligned(ap->idx_new, elem) || ap->idx_new_stride < 128) return DSA_ERR_INVALID_ARG;
+        a.idx_new = ap->idx_new;
+        a.idx_new_stride = ap->idx_new_stride;
+        a.idx_dtype = ap->idx_dtype;
+        a.idx = ap->idx;
+        a.idx_page_stride = pages->idx_page_stride;
+        a.idx_scale = ap->idx_scale;
+        a.scale_page_stride = pages->scale_page_stride;
+        a.idx_row = row_xform(ap->idx_row);
+        ++a.parts;
+    }
+    r = check_ws(ws, ws_bytes, kHdr);
+    if (r) return r;
+    if (seqs->total_q == 0) return DSA_OK;
+    a.sv = seq_view(seqs);
+    a.pv = page_view(pages);
+    a.total_q = seqs->total_q;
+    a.st = hdr(ws);
+    if (!launch_cache_append(a, ap->dtype == DSA_BF16, (cudaStream_t)stream)) return DSA_ERR_CUDA;
+    return cuda_status();
+}
+
+int dsa_paged_scores(const dsa_seqs* seqs, const dsa_pages* pages, int32_t dtype, const void* u, const float* s_row,
+                     const void* k_idx, const float* k_idx_scale, int64_t row_begin, int64_t row_count, float* scores,
+                     int64_t ld_scores, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    const Range range("dsa_paged_scores");
+    int r = check_seqs(seqs);
+    if (!r) r = check_pages(seqs, pages);
+    if (!r) r = check_idx_pool(pages, dtype, k_idx, k_idx_scale);
+    if (r) return r;
+    if (row_begin < 0 || row_count < 0 || row_begin > seqs->total_q || row_count > seqs->total_q - row_begin)
+        return DSA_ERR_INVALID_ARG;
+    if (row_count && (!u || !aligned(u, 16) || (dtype == DSA_E4M3 && !s_row))) return DSA_ERR_INVALID_ARG;
+    if (row_count && (!scores || ld_scores < seqs->max_seqlen_k)) return DSA_ERR_INVALID_ARG;
+    r = check_ws(ws, ws_bytes, kHdr);
+    if (r) return r;
+    if (row_count == 0) return DSA_OK;
+    return run_paged_scores(seqs, pages, dtype, u, s_row, k_idx, k_idx_scale, row_begin, row_count, scores, ld_scores, true,
+                            hdr(ws), (cudaStream_t)stream);
+}
+
+int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_indexer_args* ia, int32_t k, int32_t* idx,
+                     int64_t ld_idx, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    const Range range("dsa_paged_select");
+    int r = check_seqs(seqs);
+    if (!r) r = check_pages(seqs, pages);
+    if (!r) r = check_indexer(seqs, ia);
+    if (!r) r = check_idx_pool(pages, ia->dtype, ia->k_idx, ia->k_idx_scale);
+    if (r) return r;
+    if (k < 1 || (seqs->total_q && (!idx || ld_idx < k))) return DSA_ERR_INVALID_ARG;
+    const PagedSelectLayout L = paged_select_layout(seqs, ia);
+    r = check_ws(ws, ws_bytes, L.total);
+    if (r) return r;
+    if (seqs->total_q == 0) return DSA_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    uint8_t* w = (uint8_t*)ws;
+    r = run_fold(seqs, ia, w + L.u, (float*)(w + L.s_row), st);
+    float* sc = (float*)(w + L.scores);
+    for (int64_t r0 = 0; !r && r0 < seqs->total_q; r0 += L.rows) {
+        const int64_t n = seqs->total_q - r0 < L.rows ? seqs->total_q - r0 : L.rows;
+        r = run_paged_scores(seqs, pages, ia->dtype, w + L.u, (const float*)(w + L.s_row), ia->k_idx, ia->k_idx_scale, r0, n,
+                             sc, seqs->max_seqlen_k, false, hdr(ws), st);
+        if (!r)
+            r = run_topk(seqs, sc, seqs->max_seqlen_k, r0, n, k, idx + r0 * ld_idx, ld_idx, hdr(ws), st, ia->k_per_row, true);
+    }
+    return r;
+}
+
+int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_args* aa, const int32_t* idx,
+                   int64_t ld_idx, int32_t k_sel, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    const Range range("dsa_paged_attn");
+    int r = check_seqs(seqs);
+    if (!r) r = check_pages(seqs, pages);
+    if (r) return r;
+    if (!aa) return DSA_ERR_INVALID_ARG;
+    if (aa->dtype != DSA_BF16 && aa->dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+    if (aa->heads < 1) return DSA_ERR_INVALID_ARG;
+    if (seqs->total_q && (!aa->q || !aa->out || !aa->k || !aa->v)) return DSA_ERR_INVALID_ARG;
+    if (!(aa->scale >= 0.f)) return DSA_ERR_INVALID_ARG;
+    if (k_sel < 0 || (idx != nullptr) != (k_sel > 0) || (idx && ld_idx < k_sel)) return DSA_ERR_INVALID_ARG;
+    const bool bf16 = aa->dtype == DSA_BF16;
+    if (bf16) {
+        if (aa->heads > 128 || aa->dk != 576 || aa->dv != 512 || k_sel > kTcAttnMaxSel) return DSA_ERR_UNSUPPORTED;
+        if (attn_v_separate(aa)) return DSA_ERR_UNSUPPORTED;
+        if (!aligned(aa->q, 16) || !aligned(aa->k, 16) || !aligned(aa->out, 16)) return DSA_ERR_INVALID_ARG;
+        if (aa->k_stride % 8 || pages->kv_page_stride % 8 || aa->q_stride_tok % 8 || aa->q_stride_head % 8 ||
+            aa->out_stride_tok % 8 || aa->out_stride_head % 8)
+            return DSA_ERR_INVALID_ARG;
+    } else {
+        const bool okd = aa->dk % 32 == 0 && aa->dk >= 32 && aa->dk <= 128;
+        const bool okv = aa->dv % 32 == 0 && aa->dv >= 32 && aa->dv <= 128;
+        if (aa->heads > 32 || !okd || !okv) return DSA_ERR_UNSUPPORTED;
+        if (!aligned(aa->k, 4) || !aligned(aa->v, 4)) return DSA_ERR_INVALID_ARG;
+        if (!pool_ok(pages, aa->v == aa->k ? pages->kv_page_stride : pages->v_page_stride, aa->v_stride, aa->dv))
+            return DSA_ERR_INVALID_ARG;
+    }
+    if (!pool_ok(pages, pages->kv_page_stride, aa->k_stride, aa->dk)) return DSA_ERR_INVALID_ARG;
+    r = check_rows(seqs->total_q, aa->heads, aa->dk, aa->dtype, aa->q, aa->q_stride_tok, aa->q_stride_head);
+    if (!r) r = check_rows(seqs->total_q, aa->heads, aa->dv, aa->dtype, aa->out, aa->out_stride_tok, aa->out_stride_head);
+    if (r) return r;
+    const PagedAttnPlan P = paged_attn_plan(seqs, aa, k_sel);
+    r = check_ws(ws, ws_bytes, P.total);
+    if (r) return r;
+    if (seqs->total_q == 0) return DSA_OK;
+    PagedAttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.sv = seq_view(seqs);
+    a.pv = page_view(pages);
+    a.total_q = seqs->total_q;
+    a.heads = aa->heads;
+    a.dk = aa->dk;
+    a.dv = aa->dv;
+    a.q = aa->q;
+    a.q_stride_tok = aa->q_stride_tok;
+    a.q_stride_head = aa->q_stride_head;
+    a.k = aa->k;
+    a.k_stride = aa->k_stride;
+    a.k_page_stride = pages->kv_page_stride;
+    a.v = aa->v;
+    a.v_stride = aa->v_stride;
+    a.v_page_stride = aa->v == aa->k ? pages->kv_page_stride : pages->v_page_stride;
+    a.scale = aa->scale;
+    a.out = aa->out;
+    a.out_stride_tok = aa->out_stride_tok;
+    a.out_stride_head = aa->out_stride_head;
+    a.lse = aa->lse;
+    a.idx = idx;
+    a.ld_idx = ld_idx;
+    a.k_sel = k_sel;
+    a.group = P.group;
+    a.groups = P.groups;
+    a.splits = P.splits;
+    a.part_lse = (float*)((uint8_t*)ws + P.part_lse);
+    a.part_o = (float*)((uint8_t*)ws + P.part_o);
+    a.st = hdr(ws);
+    if (!(bf16 ? launch_paged_attn_tc(a, (cudaStream_t)stream) : launch_paged_attn_f32(a, (cudaStream_t)stream)))
+        return DSA_ERR_CUDA;
+    return cuda_status();
 }
 
 int dsa_sync_status(void* ws, dsa_stream_t stream, int64_t* detail) {

@@ -219,4 +219,122 @@ struct IndexerKlArgs {
 };
 bool launch_indexer_kl(const IndexerKlArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Paged cache: page table and the operators over it.
+// ---------------------------------------------------------------------------
+struct PageView {
+    const int32_t* table;  // [batch, ld_table]: page of each page_size positions
+    int64_t ld_table, num_pages;
+    int page_size;
+    int shift;             // log2(page_size), or -1
+};
+
+// Per-row transform (include/dsa.h, dsa_row_args): RMS norm of the columns
+// [0, norm_dim), then the rotation of [rope_begin, rope_begin + rope_dim).
+struct RowXform {
+    int norm_dim;
+    float eps;
+    const float* weight;   // nullable [norm_dim]
+    int rope_begin, rope_dim;
+    int interleaved;
+    const float* cos_sin;  // [rope_positions, rope_dim]: cos, then sin
+    int64_t rope_positions;
+};
+constexpr int kRowMaxDim = 2048;
+constexpr int kNormRopeBwdBlocks = 148 * 4;
+
+struct NormRopeArgs {
+    SeqView sv;
+    int64_t total_q;
+    int heads, dim;
+    RowXform ra;
+    const void* x;
+    int64_t x_stride_tok, x_stride_head;
+    const void* dy;        // backward
+    int64_t dy_stride_tok, dy_stride_head;
+    void* y;               // forward: y; backward: dx
+    int64_t y_stride_tok, y_stride_head;
+    float* dw_part;        // backward: [blocks, norm_dim] partial sums, or null
+    int64_t rows_per_warp; // set by the launcher
+    StatusHdr* st;
+};
+bool launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t s);
+int norm_rope_bwd_blocks(int64_t rows);
+bool launch_norm_rope_bwd(const NormRopeArgs& a, bool bf16, float* dw, cudaStream_t s);
+
+struct AppendArgs {
+    SeqView sv;
+    PageView pv;
+    int64_t total_q;
+    int parts;             // 1 or 2: KV row and / or indexer key
+    int dim;               // columns of a KV row
+    const void* kv_new;
+    int64_t kv_new_stride;
+    void* kv;              // KV pool (null: no KV part)
+    int64_t kv_stride, kv_page_stride;
+    RowXform kv_row;
+    const void* idx_new;   // [total_q, >= 128] of the same type as kv_new
+    int64_t idx_new_stride;
+    int idx_dtype;         // DSA_E4M3 | DSA_F32
+    void* idx;             // indexer-key pool, rows of 128
+    int64_t idx_page_stride;
+    float* idx_scale;      // DSA_E4M3
+    int64_t scale_page_stride;
+    RowXform idx_row;
+    int warp_smem;         // set by the launcher
+    StatusHdr* st;
+};
+bool launch_cache_append(const AppendArgs& a, bool bf16, cudaStream_t s);
+
+// Indexer scores over the paged indexer keys, rows [row_begin, row_begin +
+// row_count) of the packed queries.
+struct PagedScoresArgs {
+    SeqView sv;
+    PageView pv;
+    int64_t max_seqlen_q, total_q;
+    const void* u;         // folded queries [total_q, 128] (e4m3 codes or fp32)
+    const float* s_row;    // [total_q] (e4m3)
+    const void* k;         // key pool, rows of 128
+    int64_t k_page_stride;
+    const float* k_scale;  // key scales (e4m3)
+    int64_t scale_page_stride;
+    int64_t row_begin, row_count;
+    float* scores;
+    int64_t ld;
+    int64_t cols;          // columns [0, cols) are written: fill ? ld : max_seqlen_k
+    int fill;              // -inf past each row's position
+    int tiles_per_cta;     // set by the launcher
+    StatusHdr* st;
+};
+bool launch_paged_scores(const PagedScoresArgs& a, bool e4m3, cudaStream_t s);
+
+// Attention over the paged KV rows (bf16 tensor-core kernel and fp32 kernel).
+struct PagedAttnArgs {
+    SeqView sv;
+    PageView pv;
+    int64_t total_q;
+    int heads, dk, dv;
+    const void* q;
+    int64_t q_stride_tok, q_stride_head;
+    const void* k;
+    int64_t k_stride, k_page_stride;
+    const void* v;         // fp32 kernel only: its own pool (may be k's)
+    int64_t v_stride, v_page_stride;
+    float scale;
+    void* out;
+    int64_t out_stride_tok, out_stride_head;
+    float* lse;
+    const int32_t* idx;    // null: dense causal
+    int64_t ld_idx;
+    int k_sel;
+    int group;             // bf16: query tokens per work item (rows = group * heads <= 128)
+    int64_t groups;        // work items before splitting
+    int splits;            // parts of each item's key range
+    float* part_o;         // splits > 1: normalised partial outputs
+    float* part_lse;       //             and their base-2 log-sum-exp
+    StatusHdr* st;
+};
+bool launch_paged_attn_tc(const PagedAttnArgs& a, cudaStream_t s);
+bool launch_paged_attn_f32(const PagedAttnArgs& a, cudaStream_t s);
+
 }  // namespace dsa

@@ -1,0 +1,366 @@
+// norm_rope.cu -- RMS norm of every head's row and the position rotation in
+// one pass, and its gradients.
+//
+// Rows x[t, h, 0:dim] (heads may be 1, as for the shared KV row).  With
+// n = norm_dim, r = 1/sqrt(mean(x[0:n]^2) + eps):
+//     u_c = x_c r w_c (c < n),  u_c = x_c (c >= n)
+//     (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin)
+// for every pair (a, b) of the rotated columns, y_c = u_c elsewhere; the
+// angles are those of the token's position.  Backward, with g = the transposed
+// rotation of dy and x^ = x r:
+//     dx_c = r (g_c w_c - x^_c mean_n(g w x^)) (c < n),  dx_c = g_c (c >= n)
+//     dw_c = sum over rows of g_c x^_c
+//
+// Both are bound by HBM: a row is read once and written once (backward: x and
+// dy once, dx once); a group of 8 lanes (dim <= 256) or 32 lanes holds a row in
+// registers as 16-byte chunks, so the norm's reduction and the rotation need
+// no second read.  All arithmetic is fp32; the result is rounded once.
+//
+// dw is summed in a fixed order, whatever the launch: each lane sums its
+// columns over its block's rows, the block's groups are added in order, and a
+// second kernel adds the blocks' partial rows (in 64 bits).
+#include "rows.cuh"
+
+namespace dsa {
+
+constexpr int NR_THREADS = 256;
+constexpr int NR_WARPS = NR_THREADS / 32;
+
+// Token t's position row of the cos | sin table, or false (reported once).
+struct TokenPos {
+    int64_t t = -1;
+    bool ok = false;
+    const float* cs = nullptr;
+};
+DSA_DEV void token_pos(TokenPos& tp, int64_t t, const SeqView& sv, const RowXform& ra, StatusHdr* st) {
+    if (t == tp.t) return;
+    tp.t = t;
+    const RowInfo ri = row_info(sv, t);
+    tp.ok = ri.ok && (ra.rope_dim == 0 || ri.pos < ra.rope_positions);
+    if (!tp.ok) report(st, DSA_ERR_INDEX, t);
+    tp.cs = tp.ok && ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr;
+}
+
+template <class T, int G, int NC>
+__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
+    extern __shared__ __align__(16) float nr_sm[];
+    constexpr int RPW = 32 / G;  // rows per warp and step
+    const int lane = (int)lane_id(), gl = lane % G, sub = lane / G, warp = (int)warp_id();
+    float* sm = nr_sm + (warp * RPW + sub) * a.ra.rope_dim;
+    const int64_t rows = a.total_q * a.heads;
+    int64_t r = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp + sub;
+    const int64_t r_end = min(rows, r - sub + a.rows_per_warp);
+    TokenPos tp;
+    for (int64_t r0 = r - sub; r0 < r_end; r0 += RPW, r += RPW) {
+        bool live = r < r_end;
+        const T* x = nullptr;
+        T* y = nullptr;
+        if (live) {
+            const int64_t t = r / a.heads, h = r - t * a.heads;
+            token_pos(tp, t, a.sv, a.ra, a.st);
+            live = tp.ok;
+            x = (const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head;
+            y = (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head;
+        }
+        row_forward<T, G, NC>(x, y, a.ra, a.dim, tp.cs, gl, live, sm);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(NR_THREADS) norm_rope_scalar_kernel(const NormRopeArgs a) {
+    const int64_t rows = a.total_q * a.heads;
+    const int64_t step = (int64_t)gridDim.x * NR_WARPS;
+    TokenPos tp;
+    for (int64_t r = (int64_t)blockIdx.x * NR_WARPS + warp_id(); r < rows; r += step) {
+        const int64_t t = r / a.heads, h = r - t * a.heads;
+        token_pos(tp, t, a.sv, a.ra, a.st);
+        if (!tp.ok) continue;
+        row_forward_scalar<T>((const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head,
+                              (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head, a.ra, a.dim, tp.cs, (int)lane_id());
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+template <class T, int G, int NC>
+__global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_kernel(const NormRopeArgs a) {
+    extern __shared__ __align__(16) float nr_sm[];
+    constexpr int RPW = 32 / G;
+    const int lane = (int)lane_id(), gl = lane % G, sub = lane / G, warp = (int)warp_id();
+    float* sm = nr_sm + (warp * RPW + sub) * a.ra.rope_dim;
+    const int n = a.ra.norm_dim;
+    const int64_t rows = a.total_q * a.heads;
+    float acc[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+    int64_t r = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp + sub;
+    const int64_t r_end = min(rows, r - sub + a.rows_per_warp);
+    TokenPos tp;
+    for (int64_t r0 = r - sub; r0 < r_end; r0 += RPW, r += RPW) {
+        bool live = r < r_end;
+        const T *x = nullptr, *dy = nullptr;
+        T* dx = nullptr;
+        if (live) {
+            const int64_t t = r / a.heads, h = r - t * a.heads;
+            token_pos(tp, t, a.sv, a.ra, a.st);
+            live = tp.ok;
+            x = (const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head;
+            dy = (const T*)a.dy + t * a.dy_stride_tok + h * a.dy_stride_head;
+            dx = (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head;
+        }
+        float g[NC][8], xv[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (gl + G * i) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[i][e] = 0.f, xv[i][e] = 0.f;
+            if (live && c < a.dim) load8(dy + c, g[i]);
+            if (live && c < n) load8(x + c, xv[i]);
+        }
+        if (a.ra.rope_dim > 0) rotate_chunks<G, NC>(g, a.ra, tp.cs, gl, -1.f, live, sm);
+        if (n > 0) {
+            float ss = 0.f, dot = 0.f;
+            float w[NC][8];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = (gl + G * i) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
+                if (c < n) {
+                    if (a.ra.weight) {
+                        const float4 p = __ldg((const float4*)(a.ra.weight + c));
+                        const float4 q = __ldg((const float4*)(a.ra.weight + c) + 1);
+                        w[i][0] = p.x, w[i][1] = p.y, w[i][2] = p.z, w[i][3] = p.w;
+                        w[i][4] = q.x, w[i][5] = q.y, w[i][6] = q.z, w[i][7] = q.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        ss = fmaf(xv[i][e], xv[i][e], ss);
+                        dot = fmaf(g[i][e] * w[i][e], xv[i][e], dot);
+                    }
+                }
+            }
+            ss = group_sum<G>(ss);
+            dot = group_sum<G>(dot);
+            const float rstd = 1.0f / sqrtf(ss / (float)n + a.ra.eps);
+            const float k = dot * rstd / (float)n;  // mean of g w x^
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if ((gl + G * i) * 8 < n) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xh = xv[i][e] * rstd;
+                        if (live) acc[i][e] = fmaf(g[i][e], xh, acc[i][e]);
+                        g[i][e] = rstd * (g[i][e] * w[i][e] - xh * k);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (gl + G * i) * 8;
+            if (live && c < a.dim) store8(dx + c, g[i]);
+        }
+    }
+    if (!a.dw_part) return;
+    // the block's groups, added in order; each warp's RPW row groups first
+    __syncthreads();
+    float* red = nr_sm;  // [NR_WARPS][n]
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = (gl + G * i) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v = acc[i][e];
+#pragma unroll
+            for (int o = 16; o >= G; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            acc[i][e] = v;
+        }
+        if (sub == 0 && c < n) store8(red + warp * n + c, acc[i]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += NR_THREADS) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NR_WARPS; ++w) v += red[w * n + c];
+        a.dw_part[(int64_t)blockIdx.x * n + c] = v;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const NormRopeArgs a) {
+    extern __shared__ __align__(16) float nr_sm[];
+    const int lane = (int)lane_id(), warp = (int)warp_id(), n = a.ra.norm_dim;
+    const RowXform& ra = a.ra;
+    const int h = ra.rope_dim >> 1;
+    float* acc = nr_sm + warp * n;
+    for (int c = lane; c < n; c += 32) acc[c] = 0.f;
+    const int64_t rows = a.total_q * a.heads;
+    const int64_t step = (int64_t)gridDim.x * NR_WARPS;
+    TokenPos tp;
+    for (int64_t r = (int64_t)blockIdx.x * NR_WARPS + warp; r < rows; r += step) {
+        const int64_t t = r / a.heads, hd = r - t * a.heads;
+        token_pos(tp, t, a.sv, ra, a.st);
+        if (!tp.ok) continue;
+        const T* x = (const T*)a.x + t * a.x_stride_tok + hd * a.x_stride_head;
+        const T* dy = (const T*)a.dy + t * a.dy_stride_tok + hd * a.dy_stride_head;
+        T* dx = (T*)a.y + t * a.y_stride_tok + hd * a.y_stride_head;
+        auto grad = [&](int c) {  // the transposed rotation of dy at column c
+            const int o = c - ra.rope_begin;
+            if (o < 0 || o >= ra.rope_dim) return load1(dy + c);
+            const int j = ra.interleaved ? o >> 1 : (o < h ? o : o - h);
+            const bool first = ra.interleaved ? (o & 1) == 0 : o < h;
+            const int d = ra.interleaved ? 1 : h;
+            const float p = load1(dy + (first ? c + d : c - d)), co = __ldg(tp.cs + j), si = __ldg(tp.cs + h + j);
+            return first ? load1(dy + c) * co + p * si : load1(dy + c) * co - p * si;
+        };
+        float rstd = 0.f, k = 0.f;
+        if (n > 0) {
+            float ss = 0.f, dot = 0.f;
+            for (int c = lane; c < n; c += 32) {
+                const float v = load1(x + c), w = ra.weight ? __ldg(ra.weight + c) : 1.f;
+                ss = fmaf(v, v, ss);
+                dot = fmaf(grad(c) * w, v, dot);
+            }
+            ss = group_sum<32>(ss);
+            dot = group_sum<32>(dot);
+            rstd = 1.0f / sqrtf(ss / (float)n + ra.eps);
+            k = dot * rstd / (float)n;
+        }
+        for (int c = lane; c < a.dim; c += 32) {
+            const float g = grad(c);
+            if (c < n) {
+                const float xh = load1(x + c) * rstd, w = ra.weight ? __ldg(ra.weight + c) : 1.f;
+                acc[c] = fmaf(g, xh, acc[c]);  // column c of a warp is lane c % 32's alone
+                store1(dx + c, rstd * (g * w - xh * k));
+            } else {
+                store1(dx + c, g);
+            }
+        }
+    }
+    if (!a.dw_part) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += NR_THREADS) {
+        float v = 0.f;
+        for (int w = 0; w < NR_WARPS; ++w) v += nr_sm[w * n + c];
+        a.dw_part[(int64_t)blockIdx.x * n + c] = v;
+    }
+}
+
+// dw[c] = sum over the blocks' partial rows, in a fixed order: 32 strided sums
+// in 64 bits, then those in order.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int blocks, int n,
+                                                            float* __restrict__ dw) {
+    __shared__ double sm[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    double v = 0.0;
+    if (c < n)
+        for (int b = threadIdx.y; b < blocks; b += 32) v += (double)__ldg(part + (int64_t)b * n + c);
+    sm[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < n) {
+        v = 0.0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v += sm[i][threadIdx.x];
+        dw[c] = (float)v;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launch
+// ---------------------------------------------------------------------------
+template <class T, int G, int NC>
+static bool nr_launch(NormRopeArgs a, bool bwd, int blocks, cudaStream_t s) {
+    const int groups = NR_THREADS / G;
+    size_t smem = a.ra.interleaved ? 0 : (size_t)groups * a.ra.rope_dim * 4;
+    if (bwd && a.dw_part && smem < (size_t)NR_WARPS * a.ra.norm_dim * 4) smem = (size_t)NR_WARPS * a.ra.norm_dim * 4;
+    const void* fn = bwd ? (const void*)norm_rope_bwd_kernel<T, G, NC> : (const void*)norm_rope_kernel<T, G, NC>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return false;
+    if (bwd) norm_rope_bwd_kernel<T, G, NC><<<blocks, NR_THREADS, smem, s>>>(a);
+    else norm_rope_kernel<T, G, NC><<<blocks, NR_THREADS, smem, s>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+template <class T>
+static bool nr_launch_dim(const NormRopeArgs& a, bool bwd, int blocks, cudaStream_t s) {
+    if (a.dim <= 64) return nr_launch<T, 8, 1>(a, bwd, blocks, s);
+    if (a.dim <= 128) return nr_launch<T, 8, 2>(a, bwd, blocks, s);
+    if (a.dim <= 256) return nr_launch<T, 8, 4>(a, bwd, blocks, s);
+    if (a.dim <= 512) return nr_launch<T, 32, 2>(a, bwd, blocks, s);
+    if (a.dim <= 768) return nr_launch<T, 32, 3>(a, bwd, blocks, s);
+    if (a.dim <= 1024) return nr_launch<T, 32, 4>(a, bwd, blocks, s);
+    return nr_launch<T, 32, 8>(a, bwd, blocks, s);
+}
+
+static bool nr_chunked(const NormRopeArgs& a, bool bf16, bool bwd) {
+    const int64_t e = bf16 ? 8 : 4;  // elements of 16 bytes
+    auto al = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
+    bool ok = row_xform_chunked(a.ra, a.dim) && al(a.x) && al(a.y) && a.x_stride_tok % e == 0 &&
+              a.x_stride_head % e == 0 && a.y_stride_tok % e == 0 && a.y_stride_head % e == 0;
+    if (bwd) ok = ok && al(a.dy) && a.dy_stride_tok % e == 0 && a.dy_stride_head % e == 0;
+    return ok;
+}
+
+// Blocks of the backward: enough warps to fill the GPU, and no more, because
+// each block adds one partial row to dw.
+int norm_rope_bwd_blocks(int64_t rows) {
+    const int64_t want = (rows + NR_WARPS - 1) / NR_WARPS;
+    return (int)(want < kNormRopeBwdBlocks ? (want > 0 ? want : 1) : kNormRopeBwdBlocks);
+}
+
+bool launch_norm_rope(const NormRopeArgs& in, bool bf16, cudaStream_t s) {
+    NormRopeArgs a = in;
+    const int64_t rows = a.total_q * a.heads;
+    if (rows <= 0) return true;
+    if (!nr_chunked(a, bf16, false)) {
+        const int64_t blocks = (rows + NR_WARPS - 1) / NR_WARPS;
+        const unsigned g = (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
+        if (bf16) norm_rope_scalar_kernel<__nv_bfloat16><<<g, NR_THREADS, 0, s>>>(a);
+        else norm_rope_scalar_kernel<float><<<g, NR_THREADS, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess;
+    }
+    const int rpw = a.dim <= 256 ? 4 : 1;
+    int64_t per = (rows + (int64_t)148 * 64 * 4 - 1) / ((int64_t)148 * 64 * 4);  // rows a warp: a few waves of warps
+    if (per > 16) per = 16;
+    a.rows_per_warp = (int)((per + rpw - 1) / rpw * rpw);
+    const int64_t blocks = (rows + (int64_t)a.rows_per_warp * NR_WARPS - 1) / ((int64_t)a.rows_per_warp * NR_WARPS);
+    if (blocks >= ((int64_t)1 << 31)) return false;
+    return bf16 ? nr_launch_dim<__nv_bfloat16>(a, false, (int)blocks, s) : nr_launch_dim<float>(a, false, (int)blocks, s);
+}
+
+bool launch_norm_rope_bwd(const NormRopeArgs& in, bool bf16, float* dw, cudaStream_t s) {
+    NormRopeArgs a = in;
+    const int64_t rows = a.total_q * a.heads;
+    const int n = a.ra.norm_dim;
+    if (rows <= 0) return !dw || n == 0 || cudaMemsetAsync(dw, 0, (size_t)n * 4, s) == cudaSuccess;
+    int blocks = norm_rope_bwd_blocks(rows);
+    if (!dw || n == 0) a.dw_part = nullptr;
+    bool ok;
+    if (!nr_chunked(a, bf16, true)) {
+        const size_t smem = (size_t)NR_WARPS * n * 4;
+        const void* fn = bf16 ? (const void*)norm_rope_bwd_scalar_kernel<__nv_bfloat16>
+                              : (const void*)norm_rope_bwd_scalar_kernel<float>;
+        if (smem > 48 * 1024 &&
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return false;
+        if (bf16) norm_rope_bwd_scalar_kernel<__nv_bfloat16><<<blocks, NR_THREADS, smem, s>>>(a);
+        else norm_rope_bwd_scalar_kernel<float><<<blocks, NR_THREADS, smem, s>>>(a);
+        ok = cudaGetLastError() == cudaSuccess;
+    } else {
+        const int rpw = a.dim <= 256 ? 4 : 1;
+        const int64_t warps = (int64_t)blocks * NR_WARPS;
+        const int64_t per = (rows + warps - 1) / warps;
+        a.rows_per_warp = (per + rpw - 1) / rpw * rpw;
+        ok = bf16 ? nr_launch_dim<__nv_bfloat16>(a, true, blocks, s) : nr_launch_dim<float>(a, true, blocks, s);
+    }
+    if (!ok || !a.dw_part) return ok;
+    norm_rope_dw_kernel<<<(n + 31) / 32, dim3(32, 32), 0, s>>>(a.dw_part, blocks, n, dw);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace dsa

@@ -1,0 +1,328 @@
+// paged_scores.cu -- lightning-indexer scores of folded queries over the paged
+// indexer keys.
+//
+// I[t, s] = ReLU((u_t . k_s) * s_k[s] * s_row[t]) for s <= pos_t, over keys found
+// through the page table.
+//
+// FP8: keys are the M side of the MMA (128 keys a tile, one TMEM lane each) and
+// up to 16 or 128 queries of a sequence the N side, so one kernel serves decode
+// and chunks: every key row is read once per 128 queries, and a warp's stores
+// are 32 consecutive scores of one query.  Bound by HBM: a decode reads 132
+// bytes a key, a chunk writes 4 bytes a (query, key) pair; the MMA of a tile (M 128,
+// N 16 or 128, K 128) takes less time than either.
+// The key rows arrive by 16-byte cp.async, 4 rows x 128 bytes an instruction,
+// because pages may start at any row of a tile and have any size; a warp looks
+// up its 32 keys' pages with one load and shuffles the rows' places around.
+// Keys that the page table does not hold get -inf and are reported.
+#include "rows.cuh"
+
+namespace dsa {
+
+constexpr int PS_KEYS = 128;  // keys per tile
+constexpr int PS_NST = 4;     // key stages
+constexpr int PS_EPI = 4;     // epilogue warps 0..3 (TMEM lane quadrants)
+constexpr int PS_PROD = 4;    // producer warps 4..7
+constexpr int PS_MMA_WARP = 8;
+constexpr int PS_THREADS = 32 * 9;
+constexpr uint32_t PS_STAGE = PS_KEYS * 128;
+
+template <int NQ>
+struct PsSmem {
+    static constexpr uint32_t OFF_B = PS_NST * PS_STAGE;  // queries, 128-byte swizzled rows
+    static constexpr uint32_t OFF_SROW = OFF_B + NQ * 128;
+    static constexpr uint32_t OFF_BAR = OFF_SROW + NQ * 4;
+    static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // + alignment
+    static constexpr uint32_t TMEM_COLS = 2 * NQ < 32 ? 32 : 2 * NQ;
+};
+struct PsBars {
+    uint64_t full[PS_NST], empty[PS_NST];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+DSA_DEV float ps_relu(float x) {  // as the packed scores: -0 and below to +0, NaN to +inf
+    int b = __float_as_int(x);
+    b = max(b, 0);
+    b = min(b, 0x7F800000);
+    return __int_as_float(b);
+}
+
+template <int NQ>
+__global__ void __launch_bounds__(PS_THREADS) paged_scores_kernel(const PagedScoresArgs a) {
+    using Lay = PsSmem<NQ>;
+    extern __shared__ uint8_t ps_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)ps_raw + 1023) & ~(uintptr_t)1023);
+    PsBars* bars = (PsBars*)(smem + Lay::OFF_BAR);
+    float* srow = (float*)(smem + Lay::OFF_SROW);
+    const int warp = (int)warp_id(), lane = (int)lane_id();
+    volatile int* abort = &bars->abort;
+    StatusHdr* st = a.st;
+
+    // this CTA: queries [t_first, t_first + nrows) of sequence b, key tiles [t_lo, t_hi)
+    const int64_t nblk = (a.max_seqlen_q + NQ - 1) / NQ;
+    const int64_t tiles = (a.cols + PS_KEYS - 1) / PS_KEYS;
+    const int64_t nsplit = (tiles + a.tiles_per_cta - 1) / a.tiles_per_cta;
+    const int64_t u = blockIdx.x / nsplit, split = blockIdx.x - u * nsplit;
+    const int b = (int)(u / nblk);
+    const int64_t q0 = __ldg(a.sv.cu_q + b), q1 = __ldg(a.sv.cu_q + b + 1);
+    const int64_t lk = __ldg(a.sv.cu_k + b + 1) - __ldg(a.sv.cu_k + b), lq = q1 - q0;
+    const int64_t i0 = (u - b * nblk) * NQ;
+    if (i0 >= lq) return;
+    const int64_t t_first = q0 + i0;
+    const int nrows = (int)min((int64_t)NQ, min(lq - i0, a.total_q - t_first));
+    const int64_t pos_first = lk - lq + i0;  // position of block row 0
+    if (t_first < 0 || pos_first < 0) {      // the batch's description is inconsistent
+        if (threadIdx.x == 0) report(st, DSA_ERR_INDEX, t_first);
+        if (t_first < 0) return;
+    }
+    // rows of the block that are asked for (and have a position)
+    const int r_lo = (int)max(max((int64_t)0, -pos_first), a.row_begin - t_first);
+    const int r_hi = (int)min((int64_t)nrows, a.row_begin + a.row_count - t_first);
+    if (r_lo >= r_hi) return;
+    const int64_t pos_last = pos_first + r_hi - 1;           // of the last row asked for
+    const int64_t t_lo = split * a.tiles_per_cta;
+    const int64_t t_hi = min(tiles, t_lo + a.tiles_per_cta);
+    const int64_t t_act = max(t_lo, min(t_hi, pos_last / PS_KEYS + 1));  // tiles with keys some row sees
+    if (t_act == t_lo && !a.fill) return;
+
+    const uint32_t s_a = smem_u32(smem), s_b = smem_u32(smem + Lay::OFF_B);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < PS_NST; ++i) {
+            mbar_init(smem_u32(&bars->full[i]), PS_PROD * 32);
+            mbar_init(smem_u32(&bars->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->acc_full[i]), 1);
+            mbar_init(smem_u32(&bars->acc_empty[i]), PS_EPI);
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == PS_MMA_WARP) {
+        tmem_alloc(smem_u32(&bars->tmem_base), Lay::TMEM_COLS);
+        tmem_relinquish();  // several CTAs share an SM
+    }
+    // the queries, 16 bytes a thread; rows past the block are zero
+    for (int i = threadIdx.x; i < NQ * 8; i += PS_THREADS) {
+        const int r = i >> 3, c = i & 7;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nrows) v = __ldg((const uint4*)((const uint8_t*)a.u + (t_first + r) * 128 + c * 16));
+        *(uint4*)(smem + Lay::OFF_B + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+    }
+    for (int i = threadIdx.x; i < NQ; i += PS_THREADS) srow[i] = i < nrows ? __ldg(a.s_row + t_first + i) : 0.f;
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    if (warp >= PS_EPI && warp < PS_MMA_WARP) {
+        // ================= producers =================
+        const int pw = warp - PS_EPI, sub = lane >> 3, chunk = lane & 7;
+        const uint8_t* pool = (const uint8_t*)a.k;
+        auto place = [&](int64_t tile) -> int64_t {  // byte offset of this lane's key, -1: not loaded
+            const int64_t s = tile * PS_KEYS + pw * 32 + lane;
+            if (tile >= t_act || s > pos_last) return -1;
+            const PageRef pr = page_of(a.pv, b, s);
+            return pr.page < 0 ? -1 : pr.page * a.k_page_stride + (int64_t)pr.slot * 128;
+        };
+        int64_t nxt = place(t_lo);
+        uint32_t g = 0;
+        for (int64_t tile = t_lo; tile < t_act; ++tile, ++g) {
+            const int64_t cur = nxt;
+            nxt = place(tile + 1);
+            const uint32_t s = g % PS_NST;
+            if (!wait_warp(smem_u32(&bars->empty[s]), ((g / PS_NST) & 1) ^ 1, abort, st, 0x4101)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = i * 4 + sub;
+                const int64_t off = __shfl_sync(0xffffffffu, cur, key);
+                const int r = pw * 32 + key;
+                if (off >= 0) cp_async16(s_a + s * PS_STAGE + r * 128 + ((chunk ^ (r & 7)) << 4), pool + off + chunk * 16);
+            }
+            cp_async_arrive(smem_u32(&bars->full[s]));
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == PS_MMA_WARP) {
+        // ================= MMA issuer =================
+        constexpr uint32_t idesc = idesc_make(0, 0, false, PS_KEYS, NQ);
+        uint32_t g = 0;
+        for (int64_t tile = t_lo; tile < t_act; ++tile, ++g) {
+            const uint32_t s = g % PS_NST, ab = g & 1;
+            if (!wait_warp(smem_u32(&bars->full[s]), (g / PS_NST) & 1, abort, st, 0x4201)) break;
+            if (!wait_warp(smem_u32(&bars->acc_empty[ab]), ((g >> 1) & 1) ^ 1, abort, st, 0x4202)) break;
+            fence_proxy_async();
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_fp8_ss(tmem + ab * NQ, sdesc_sw128(s_a + s * PS_STAGE + ks * 32, 16, 1024),
+                               sdesc_sw128(s_b + ks * 32, 16, 1024), idesc, ks > 0 ? 1u : 0u);
+                mma_commit(smem_u32(&bars->empty[s]));
+                mma_commit(smem_u32(&bars->acc_full[ab]));
+            }
+            __syncwarp();
+        }
+        if (*abort && lane == 0) {
+            mma_commit(smem_u32(&bars->drain));
+            mbar_wait(smem_u32(&bars->drain), 0, nullptr, st, 0x4203, 1ll << 28);
+        }
+    } else {
+        // ================= epilogue: one thread per key =================
+        float* out = a.scores + (t_first - a.row_begin) * a.ld;
+        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        const float none = a.fill ? -INFINITY : 0.f;  // the selection's own scores are never negative
+        auto scale_of = [&](int64_t tile, bool& ok) -> float {
+            const int64_t s = tile * PS_KEYS + warp * 32 + lane;
+            ok = true;
+            if (tile >= t_act || s > pos_last) return 0.f;
+            const PageRef pr = page_of(a.pv, b, s);
+            ok = pr.page >= 0;
+            if (!ok) {
+                report(st, DSA_ERR_INDEX, t_first);
+                return 0.f;
+            }
+            return __ldg(a.k_scale + pr.page * a.scale_page_stride + pr.slot);
+        };
+        bool nok;
+        float nks = scale_of(t_lo, nok);
+        uint32_t g = 0;
+        bool ok = true;
+        for (int64_t tile = t_lo; ok && tile < t_act; ++tile, ++g) {
+            const uint32_t ab = g & 1;
+            const float ks = nks;
+            const bool have = nok;
+            nks = scale_of(tile + 1, nok);
+            if (!wait_warp(smem_u32(&bars->acc_full[ab]), (g >> 1) & 1, abort, st, 0x4301)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int64_t s = tile * PS_KEYS + warp * 32 + lane;
+            const bool in = s < a.cols;
+            for (int c0 = 0; c0 < r_hi; c0 += 16) {
+                uint32_t acc[16];
+                tmem_ld16(tmem + lane_off + ab * NQ + c0, acc);
+                tmem_wait_ld();
+                if (c0 + 16 >= r_hi) {  // the last columns read: hand the accumulator back
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[ab]));
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int r = c0 + e;
+                    if (r >= r_lo && r < r_hi) {
+                        const float x = ps_relu(__fmul_rn(__fmul_rn(__uint_as_float(acc[e]), ks), srow[r]));
+                        const bool seen = s <= pos_first + r;
+                        if (in && (seen || a.fill)) out[(int64_t)r * a.ld + s] = seen && have ? x : none;
+                    }
+                }
+            }
+        }
+        if (a.fill)  // tiles past every row's position
+            for (int64_t tile = t_act; tile < t_hi; ++tile) {
+                const int64_t s = tile * PS_KEYS + warp * 32 + lane;
+                if (s < a.cols)
+                    for (int r = r_lo; r < r_hi; ++r) out[(int64_t)r * a.ld + s] = -INFINITY;
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == PS_MMA_WARP) tmem_dealloc(tmem, Lay::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// fp32 keys (the small fp32 configuration): 8 lanes a key, 16 columns each,
+// one query a block; exact fp32 products and sums.
+// ---------------------------------------------------------------------------
+constexpr int PSF_KEYS = 256;  // keys per block
+
+__global__ void __launch_bounds__(256) paged_scores_f32_kernel(const PagedScoresArgs a) {
+    const int64_t t = a.row_begin + blockIdx.y;
+    const RowInfo ri = row_info(a.sv, t);
+    if (!ri.ok) {
+        if (threadIdx.x == 0) report(a.st, DSA_ERR_INDEX, t);
+        return;
+    }
+    const int sub = threadIdx.x & 7;
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldg((const float4*)((const float*)a.u + t * 128 + sub * 16) + i);
+        q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
+    }
+    float* out = a.scores + (int64_t)blockIdx.y * a.ld;
+    const int64_t s_end = min((int64_t)(blockIdx.x + 1) * PSF_KEYS, a.cols);
+    for (int64_t s0 = (int64_t)blockIdx.x * PSF_KEYS; s0 < s_end; s0 += 32) {
+        const int64_t s = s0 + (threadIdx.x >> 3);
+        float acc = 0.f;
+        bool have = true;
+        if (s <= ri.pos && s < s_end) {
+            const PageRef pr = page_of(a.pv, ri.b, s);
+            have = pr.page >= 0;
+            if (have) {
+                const float4* k = (const float4*)((const float*)a.k + pr.page * a.k_page_stride + (int64_t)pr.slot * 128 +
+                                                  sub * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = __ldg(k + i);
+                    acc = fmaf(q[4 * i], v.x, acc);
+                    acc = fmaf(q[4 * i + 1], v.y, acc);
+                    acc = fmaf(q[4 * i + 2], v.z, acc);
+                    acc = fmaf(q[4 * i + 3], v.w, acc);
+                }
+            } else {
+                report(a.st, DSA_ERR_INDEX, t);
+            }
+        }
+        acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+        acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+        acc += __shfl_xor_sync(0xffffffffu, acc, 4);
+        if (sub == 0 && s < s_end) {
+            const bool seen = s <= ri.pos;
+            if (seen || a.fill) out[s] = seen && have ? ps_relu(acc) : a.fill ? -INFINITY : 0.f;
+        }
+    }
+}
+
+template <int NQ>
+static bool ps_launch(PagedScoresArgs a, cudaStream_t s) {
+    const int64_t tiles = (a.cols + PS_KEYS - 1) / PS_KEYS;
+    const int64_t units = (a.max_seqlen_q + NQ - 1) / NQ * a.sv.batch;
+    if (tiles <= 0 || units <= 0) return true;
+    // key tiles a CTA: about four CTAs for every two that are resident on an SM, and
+    // at least four tiles, so that the start of a CTA is hidden by its neighbour
+    int64_t per = (tiles * units + 148 * 8 - 1) / (148 * 8);
+    per = per < 4 ? 4 : per > 64 ? 64 : per;
+    a.tiles_per_cta = (int)per;
+    const int64_t grid = (tiles + per - 1) / per * units;
+    if (grid >= ((int64_t)1 << 31)) return false;
+    if (cudaFuncSetAttribute(paged_scores_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)PsSmem<NQ>::SMEM) != cudaSuccess)
+        return false;
+    paged_scores_kernel<NQ><<<(unsigned)grid, PS_THREADS, PsSmem<NQ>::SMEM, s>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+bool launch_paged_scores(const PagedScoresArgs& a, bool e4m3, cudaStream_t s) {
+    if (a.row_count <= 0 || a.cols <= 0) return true;
+    if (e4m3) return a.max_seqlen_q <= 16 ? ps_launch<16>(a, s) : ps_launch<128>(a, s);
+    const int64_t gx = (a.cols + PSF_KEYS - 1) / PSF_KEYS;
+    // rows on the grid's second axis, at most 65535 a launch
+    for (int64_t r = 0; r < a.row_count; r += 65535) {
+        PagedScoresArgs p = a;
+        p.row_begin = a.row_begin + r;
+        p.row_count = a.row_count - r < 65535 ? a.row_count - r : 65535;
+        p.scores = a.scores + r * a.ld;
+        paged_scores_f32_kernel<<<dim3((unsigned)gx, (unsigned)p.row_count), 256, 0, s>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return false;
+    }
+    return true;
+}
+
+}  // namespace dsa

@@ -15,7 +15,8 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_INDEX = range(7)
 DSA_F32, DSA_BF16, DSA_E4M3 = 0, 1, 2
-DSA_OP_FOLD, DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_ATTN, DSA_OP_FORWARD, DSA_OP_FORWARD_HOST = range(6)
+(DSA_OP_FOLD, DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_ATTN, DSA_OP_FORWARD, DSA_OP_FORWARD_HOST,
+ DSA_OP_NORM_ROPE_BWD, DSA_OP_PAGED_SELECT, DSA_OP_PAGED_ATTN) = range(9)
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libdsa.so not built ({LIB_PATH}); run python -m sparse_attention_11_b200.build")
@@ -40,7 +41,24 @@ class dsa_attn_args(ctypes.Structure):
                 ("scale", _F), ("out", _P), ("out_stride_tok", _I64), ("out_stride_head", _I64), ("lse", _P)]
 
 
+class dsa_row_args(ctypes.Structure):
+    _fields_ = [("norm_dim", _I32), ("eps", _F), ("weight", _P), ("rope_begin", _I32), ("rope_dim", _I32),
+                ("rope_interleaved", _I32), ("cos_sin", _P), ("rope_positions", _I64)]
+
+
+class dsa_pages(ctypes.Structure):
+    _fields_ = [("page_size", _I32), ("num_pages", _I64), ("table", _P), ("ld_table", _I64), ("kv_page_stride", _I64),
+                ("v_page_stride", _I64), ("idx_page_stride", _I64), ("scale_page_stride", _I64)]
+
+
+class dsa_append_args(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("dim", _I32), ("kv_new", _P), ("kv_new_stride", _I64), ("kv", _P), ("kv_stride", _I64),
+                ("kv_row", ctypes.POINTER(dsa_row_args)), ("idx_dtype", _I32), ("idx_new", _P), ("idx_new_stride", _I64),
+                ("idx", _P), ("idx_scale", _P), ("idx_row", ctypes.POINTER(dsa_row_args))]
+
+
 _S, _IA, _AA = ctypes.POINTER(dsa_seqs), ctypes.POINTER(dsa_indexer_args), ctypes.POINTER(dsa_attn_args)
+_RA, _PG, _AP = ctypes.POINTER(dsa_row_args), ctypes.POINTER(dsa_pages), ctypes.POINTER(dsa_append_args)
 _lib.dsa_status_string.restype = ctypes.c_char_p
 _lib.dsa_status_string.argtypes = [ctypes.c_int]
 _lib.dsa_version.restype = ctypes.c_int
@@ -58,6 +76,13 @@ _lib.dsa_forward.argtypes = [_S, _IA, _AA, _I32, _P, _I64, _P, _SZ, _P]
 _lib.dsa_forward_host.argtypes = [_S, _IA, _AA, _I32, _P, _I64, _P, _SZ, _P, _P, _P]
 _lib.dsa_select.argtypes = [_S, _IA, _I32, _P, _I64, _P, _SZ, _P]
 _lib.dsa_select_noalloc.argtypes = [_S, _IA, _I32, _P, _I64, _P]
+_lib.dsa_norm_rope.argtypes = [_S, _RA, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P]
+_lib.dsa_norm_rope_bwd.argtypes = [_S, _RA, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _SZ,
+                                   _P]
+_lib.dsa_cache_append.argtypes = [_S, _PG, _AP, _P, _SZ, _P]
+_lib.dsa_paged_scores.argtypes = [_S, _PG, _I32, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _SZ, _P]
+_lib.dsa_paged_select.argtypes = [_S, _PG, _IA, _I32, _P, _I64, _P, _SZ, _P]
+_lib.dsa_paged_attn.argtypes = [_S, _PG, _AA, _P, _I64, _I32, _P, _SZ, _P]
 _lib.dsa_sync_status.argtypes = [_P, _P, ctypes.POINTER(_I64)]
 _lib.dsa_selftest_wait_timeout.argtypes = [_P, _SZ, _I64, _P]
 for _f in ("dsa_workspace_size", "dsa_fold", "dsa_index_scores", "dsa_topk", "dsa_sparse_attn", "dsa_sparse_attn_bwd",
@@ -65,13 +90,16 @@ for _f in ("dsa_workspace_size", "dsa_fold", "dsa_index_scores", "dsa_topk", "ds
            "dsa_forward",
            "dsa_forward_host",
            "dsa_select", "dsa_select_noalloc",
+           "dsa_norm_rope", "dsa_norm_rope_bwd", "dsa_cache_append", "dsa_paged_scores", "dsa_paged_select",
+           "dsa_paged_attn",
            "dsa_sync_status", "dsa_selftest_wait_timeout"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 EXPORTED = ("dsa_status_string", "dsa_version", "dsa_workspace_size", "dsa_fold", "dsa_index_scores", "dsa_topk",
             "dsa_sparse_attn", "dsa_sparse_attn_bwd", "dsa_attn_target", "dsa_indexer_kl", "dsa_forward",
             "dsa_forward_host", "dsa_select",
-            "dsa_select_noalloc", "dsa_sync_status",
+            "dsa_select_noalloc", "dsa_norm_rope", "dsa_norm_rope_bwd", "dsa_cache_append", "dsa_paged_scores",
+            "dsa_paged_select", "dsa_paged_attn", "dsa_sync_status",
             "dsa_selftest_wait_timeout")
 
 
@@ -246,6 +274,209 @@ def dsa_select_noalloc(seqs, ia, k, idx):
     memory): synchronous, returns nothing, raises DsaError on any status."""
     _check(_lib.dsa_select_noalloc(ctypes.byref(seqs.c), ctypes.byref(ia), k, _ptr(idx), idx.stride(0), _stream()),
            "dsa_select_noalloc")
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype(t):
+    _need(t.dtype in (torch.bfloat16, torch.float32), "bfloat16 or float32 expected")
+    return DSA_BF16 if t.dtype == torch.bfloat16 else DSA_F32
+
+
+def _here(t):
+    """Refuse tensors of another device than the current one, whose stream the
+    call would use."""
+    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), "tensors must be on the current CUDA device")
+
+
+def rope_table(positions, dim, base=10000.0, device="cuda"):
+    """cos | sin [positions, dim] (float32) of pos / base^(2i/dim), with the
+    angles in 64 bits: a plan-time table for row_args (any other angles will do)."""
+    f = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def row_args(norm_dim=0, weight=None, eps=1e-6, rope_begin=0, rope_dim=0, cos_sin=None, interleaved=True):
+    """The per-row transform of queries and keys: RMS norm of the columns
+    [0, norm_dim) (weight: float32 [norm_dim] or None for ones), then the rotation
+    of [rope_begin, rope_begin + rope_dim) by the position's row of cos_sin
+    (float32 [positions, rope_dim], cosines then sines); pairs (2i, 2i+1) when
+    interleaved, else (i, i + rope_dim/2)."""
+    if weight is not None:
+        _need(weight.dtype == torch.float32 and weight.is_contiguous() and weight.numel() == norm_dim,
+              "weight: contiguous float32 [norm_dim]")
+    if rope_dim:
+        _need(cos_sin is not None and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2
+              and cos_sin.shape[1] == rope_dim, "cos_sin: contiguous float32 [positions, rope_dim]")
+    a = dsa_row_args(norm_dim, eps, weight.data_ptr() if weight is not None else None, rope_begin, rope_dim,
+                     int(interleaved), cos_sin.data_ptr() if rope_dim else None, cos_sin.shape[0] if rope_dim else 0)
+    a._keep = (weight, cos_sin)
+    return a
+
+
+class Pages:
+    """A page table and its pools: table int32 [batch, pages per sequence];
+    kv [num_pages, page_size, >=dk], v (its own pool, or None), idx [num_pages,
+    page_size, 128] (uint8 e4m3 codes or float32), idx_scale float32 [num_pages,
+    page_size].  Pools may be strided by page; keeps the tensors alive."""
+
+    def __init__(self, table, kv=None, v=None, idx=None, idx_scale=None):
+        _need(table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1, "table: int32 [batch, n]")
+        pools = [p for p in (kv, v, idx, idx_scale) if p is not None]
+        _need(pools, "a page table needs a pool")
+        n, size = pools[0].shape[:2]
+        for p in pools:
+            _need(p.shape[0] == n and p.shape[1] == size, "pools of one table have the same pages")
+            _need(p.device == table.device, "pools and table are on one device")
+        for p in (kv, v):
+            _need(p is None or (p.dim() == 3 and p.stride(2) == 1), "kv: [pages, page_size, columns]")
+            _need(p is None or p.dtype in (torch.bfloat16, torch.float32), "kv: bfloat16 or float32")
+        _need(kv is None or v is None or kv.dtype == v.dtype, "kv and v have one type")
+        _need(idx is None or (idx.dim() == 3 and idx.shape[2] == 128 and idx.stride(2) == 1
+                              and (idx.stride(1) == 128 or size == 1)
+                              and idx.dtype in (torch.uint8, torch.float32)),
+              "idx: uint8 or float32 [pages, page_size, 128], rows contiguous")
+        _need(idx_scale is None or (idx_scale.dim() == 2 and idx_scale.dtype == torch.float32
+                                    and (idx_scale.stride(1) == 1 or size == 1)), "idx_scale: float32 [pages, page_size]")
+        self.table, self.kv, self.v, self.idx, self.idx_scale = table, kv, v, idx, idx_scale
+
+        def page(p):
+            return 0 if p is None else p.stride(0)
+
+        self.c = dsa_pages(size, n, table.data_ptr(), table.stride(0), page(kv), page(v), page(idx), page(idx_scale))
+
+
+def append_args(pages, kv_new=None, kv_row=None, idx_new=None, idx_row=None):
+    """Rows to append to the pools of `pages`: kv_new [T, dim] (of the KV pool's
+    type) and / or idx_new [T, 128], each with its row_args or None."""
+    _need(kv_new is not None or idx_new is not None, "nothing to append")
+    a = dsa_append_args()
+    a.dtype = _dtype(kv_new if kv_new is not None else idx_new)
+    if kv_new is not None:
+        _need(pages.kv is not None and kv_new.dtype == pages.kv.dtype, "kv_new has the KV pool's type")
+        _need(kv_new.dim() == 2 and kv_new.stride(1) == 1 and kv_new.shape[1] <= pages.kv.shape[2], "kv_new: [T, dim]")
+        a.dim, a.kv_new, a.kv_new_stride = kv_new.shape[1], kv_new.data_ptr(), kv_new.stride(0)
+        a.kv, a.kv_stride = pages.kv.data_ptr(), pages.kv.stride(1)
+        a.kv_row = ctypes.pointer(kv_row) if kv_row is not None else None
+    if idx_new is not None:
+        _need(pages.idx is not None and _dtype(idx_new) == a.dtype, "idx_new has kv_new's type")
+        _need(idx_new.dim() == 2 and idx_new.stride(1) == 1 and idx_new.shape[1] == 128, "idx_new: [T, 128]")
+        a.idx_dtype = DSA_E4M3 if pages.idx.dtype == torch.uint8 else DSA_F32
+        a.idx_new, a.idx_new_stride, a.idx = idx_new.data_ptr(), idx_new.stride(0), pages.idx.data_ptr()
+        a.idx_scale = pages.idx_scale.data_ptr() if pages.idx_scale is not None else None
+        a.idx_row = ctypes.pointer(idx_row) if idx_row is not None else None
+    a._keep = (pages, kv_new, kv_row, idx_new, idx_row)
+    return a
+
+
+def paged_attn_args(pages, q, scale, out, lse=None):
+    """attn_args over the pools of `pages`: q [T,H,dk], out [T,H,dv]; V is the V
+    pool, or the first dv columns of the KV rows where there is none."""
+    kv, v = pages.kv, pages.v if pages.v is not None else pages.kv
+    _need(kv is not None and q.dtype == kv.dtype and out.dtype == q.dtype, "q, out and the KV pool have one type")
+    _need(q.shape[2] <= kv.shape[2] and out.shape[2] <= v.shape[2] and q.shape[:2] == out.shape[:2], "q [T,H,dk], out [T,H,dv]")
+    _need(q.stride(2) == 1 and out.stride(2) == 1, "q and out: contiguous rows")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2]),
+          "lse: contiguous float32 [T,H]")
+    a = dsa_attn_args(_dtype(q), q.shape[1], q.shape[2], out.shape[2], q.data_ptr(), q.stride(0), q.stride(1),
+                      kv.data_ptr(), kv.stride(1), v.data_ptr(), v.stride(1), float(scale), out.data_ptr(), out.stride(0),
+                      out.stride(1), lse.data_ptr() if lse is not None else None)
+    a._keep = (pages, q, out, lse)
+    return a
+
+
+def _rows_of(seqs, t, dtype):
+    _need(t.dim() == 3 and t.shape[0] >= seqs.total_q and t.stride(2) == 1 and t.dtype == dtype,
+          "rows: [T, heads, dim] of one type, contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def dsa_norm_rope(seqs, ra, x, y, ws):
+    """y[t,h,:] = the transform ra (row_args or None) of x[t,h,:] at token t's
+    position; x, y [T,H,dim] bfloat16 or float32 (y may be x)."""
+    _here(x)
+    _check(_lib.dsa_norm_rope(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(x), x.shape[1],
+                              x.shape[2], *_rows_of(seqs, x, x.dtype), *_rows_of(seqs, y, x.dtype), _ptr(ws), ws.numel(),
+                              _stream()), "dsa_norm_rope")
+
+
+def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
+    """Backward of dsa_norm_rope: d_x [T,H,dim] (x's type) and d_weight (float32
+    [norm_dim] or None) are written from x and d_y.  ws of
+    dsa_workspace_size(DSA_OP_NORM_ROPE_BWD, seqs, norm_dim) bytes."""
+    _here(d_y)
+    _need(x.shape == d_y.shape == d_x.shape, "x, d_y and d_x have one shape")
+    _need(d_weight is None or (d_weight.dtype == torch.float32 and d_weight.is_contiguous()
+                               and d_weight.numel() == (ra.norm_dim if ra is not None else 0)),
+          "d_weight: contiguous float32 [norm_dim]")
+    _check(_lib.dsa_norm_rope_bwd(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(d_y),
+                                  d_y.shape[1], d_y.shape[2], *_rows_of(seqs, x, d_y.dtype),
+                                  *_rows_of(seqs, d_y, d_y.dtype), *_rows_of(seqs, d_x, d_y.dtype), _ptr(d_weight), _ptr(ws),
+                                  ws.numel(), _stream()), "dsa_norm_rope_bwd")
+
+
+def dsa_cache_append(seqs, pages, ap, ws):
+    """Append the queries' tokens (append_args) to the paged cache at their
+    positions.  seqs holds the lengths after the append."""
+    _here(pages.table)
+    _need(pages.table.shape[0] >= seqs.c.batch, "the table has a row per sequence")
+    for t in ap._keep[1], ap._keep[3]:
+        _need(t is None or t.shape[0] >= seqs.total_q, "a row per query token")
+    _check(_lib.dsa_cache_append(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ap), _ptr(ws), ws.numel(),
+                                 _stream()), "dsa_cache_append")
+
+
+def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
+    """Indexer scores of folded queries (u, s_row from dsa_fold) over the paged
+    indexer keys; scores float32 [row_count, >= max_seqlen_k], -inf past a row's
+    position.  dsa_topk selects from them."""
+    _here(u)
+    _need(pages.idx is not None and pages.table.shape[0] >= seqs.c.batch, "an indexer-key pool, a table row per sequence")
+    _need(u.dtype == pages.idx.dtype and u.is_contiguous() and u.shape[0] >= seqs.total_q and u.shape[1] == 128,
+          "u: contiguous [T, 128] of the pool's type")
+    _need(scores.dtype == torch.float32 and scores.stride(1) == 1 and scores.shape[0] >= row_count
+          and scores.shape[1] >= seqs.max_seqlen_k, "scores: float32 [row_count, >= max_seqlen_k]")
+    fp8 = u.dtype == torch.uint8
+    _check(_lib.dsa_paged_scores(ctypes.byref(seqs.c), ctypes.byref(pages.c), DSA_E4M3 if fp8 else DSA_F32, _ptr(u),
+                                 _ptr(s_row), _ptr(pages.idx), _ptr(pages.idx_scale) if fp8 else None, row_begin, row_count,
+                                 _ptr(scores), scores.shape[1] if scores.shape[0] == 1 else scores.stride(0), _ptr(ws),
+                                 ws.numel(), _stream()), "dsa_paged_scores")
+
+
+def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
+    """indexer_args over the indexer-key pool of `pages`."""
+    _need(pages.idx is not None and pages.idx.dtype == q_idx.dtype, "q_idx has the indexer-key pool's type")
+    return indexer_args(q_idx, q_idx_scale, w_index, pages.idx, pages.idx_scale if q_idx.dtype == torch.uint8 else None,
+                        k_per_row)
+
+
+def dsa_paged_select(seqs, pages, ia, k, idx, ws):
+    """dsa_select over the paged indexer keys (ia from paged_indexer_args).  ws
+    of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
+    _here(idx)
+    _need(pages.table.shape[0] >= seqs.c.batch and idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
+          and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k], a table row per sequence")
+    _check(_lib.dsa_paged_select(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ia), k, _ptr(idx),
+                                 max(idx.stride(0), k), _ptr(ws), ws.numel(), _stream()), "dsa_paged_select")
+
+
+def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
+    """Attention of the queries over the paged KV rows (aa from
+    paged_attn_args): dense causal with idx None and k_sel 0, else over idx
+    int32 [T, >= k_sel] of local positions (-1 unused).  ws of
+    dsa_workspace_size(DSA_OP_PAGED_ATTN, seqs, k_sel, None, aa) bytes."""
+    _here(pages.table)
+    _need(pages.table.shape[0] >= seqs.c.batch and aa._keep[1].shape[0] >= seqs.total_q,
+          "a table row per sequence, a q row per token")
+    _need(idx is None or (idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q and idx.stride(1) == 1
+                          and idx.shape[1] >= k_sel), "idx: int32 [T, >= k_sel]")
+    _check(_lib.dsa_paged_attn(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(aa), _ptr(idx),
+                               max(idx.stride(0), k_sel) if idx is not None else 0, k_sel, _ptr(ws), ws.numel(), _stream()),
+           "dsa_paged_attn")
 
 
 def dsa_sync_status(ws):
