@@ -1111,7 +1111,6 @@ int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_app
         a.kv_stride = ap->kv_stride;
         a.kv_page_stride = pages->kv_page_stride;
         a.kv_row = row_xform(ap->kv_row);
-        ++a.parts;
     }
     if (ap->idx_new) {
         r = check_row(ap->idx_row, 128);
@@ -1126,7 +1125,6 @@ int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_app
         a.idx_scale = ap->idx_scale;
         a.scale_page_stride = pages->scale_page_stride;
         a.idx_row = row_xform(ap->idx_row);
-        ++a.parts;
     }
     r = check_ws(ws, ws_bytes, kHdr);
     if (r) return r;

@@ -3,27 +3,58 @@
 // layout (up to 128 heads share one KV row of 512 latent + 64 rope columns, V is
 // the latent part), dense causal or over each query's selected positions.
 //
-// The tile pipeline is that of attn_tc.cu (a CTA pair splits the contraction
-// and the output columns, exchanging partial scores and probabilities); what
-// differs:
-//   * Work items.  An item is a group of query rows and a part of their keys.  A
-//     selection's item is one query; a dense item is up to 128 / heads
-//     consecutive tokens of a sequence, so that a rank that holds few heads
-//     still fills the 128 rows of the MMA (row r: token r / heads, head
-//     r % heads; each row masks its own causal limit).
-//   * Parts.  With fewer items than CTA pairs the keys of an item are split;
-//     the parts leave normalised fp32 rows and their log-sum-exp in the
-//     workspace and attn_paged_combine_kernel joins them.
-//   * Rows through the page table, looked up one tile ahead.  Slots that hold no row
-//     are filled with zeros, so a masked probability never meets a stray NaN.
-//   * The running maximum is a true one where it moves (see stage B), so scores
-//     whose two partial sums are large and of opposite sign lose nothing.
-#include "attn_pair.cuh"
+// Split.  O (128 rows x 512 fp32) fills a whole SM's tensor memory, so an item's
+// output columns are halved between two CTAs.  Each computes all of
+// S = Q K^T (128 x 576 by 576 x 64 a tile) and its 128 x 256 half of O += P V.
+// Nothing is exchanged: the CTAs are independent.  The price is computing S
+// twice, 1344 tensor cycles a tile; halving the contraction between the CTAs of a
+// cluster (as attn_tc.cu does) costs an exchange of partial scores and
+// probabilities through distributed shared memory, and measured 2590 us here
+// (two chunks of 300-700 tokens over 3000-5000 keys, 128 heads) against 2095 us.
+//
+// Work items.  An item is a group of query rows and a part of their keys.  A
+// selection's item is one query; a dense item is up to 128 / heads consecutive
+// tokens of a sequence, so that a rank that holds few heads still fills the 128
+// rows of the MMA (row r: token r / heads, head r % heads; each row masks its
+// own causal limit).  With fewer items than SM pairs the keys of an item are
+// split into parts, which leave normalised fp32 rows and their log-sum-exp in
+// the workspace for attn_paged_combine_kernel to join.  The grid is persistent:
+// CTA c takes units c, c + grid, ... (unit = item and half).
+//
+// Pipeline of a 64-key tile g.  A tile's nine 64-column blocks are held in two
+// parts: the four that are also V (three stages), and the five that only S reads
+// (one stage in two groups, each refilled as soon as its MMAs are done).  The MMA
+// warp issues
+//     S over group 0 | S over group 1 and the V blocks | PV of g - 1
+// so that the softmax of g - 1 runs under S(g), S(g + 1) finds its accumulator read
+// while PV(g - 1) runs, and every load has 1300 cycles or more.
+//
+// Measured on this layout (one SM, cycles): tcgen05.mma M 128, K 16 with A in
+// tensor memory: 32 at N 64, issued under elect.sync (45 under lane == 0);
+// with A in shared memory 48 (its reads of A and B at 128 bytes a cycle); N 256:
+// 128.  So S is 24 x 32 + 12 x 48 = 1344 and PV 512.  Rows gathered by 16-byte
+// cp.async reach 70 bytes a cycle (1040 a tile), gather4 TMA 8 to 22.
+//
+// Tensor memory: O [0, 256), S [256, 320), Q [320, 512) (six of its nine
+// 64-column blocks; the other three are read from shared memory).
+// Warps: 0-7 softmax (two threads a row, 32 keys each), 8-11 Q loads and the
+// epilogue (thread <-> row), 12-18 producers, 19 MMA.
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace dsa {
 
-constexpr int PA_NST = 3, PA_NPB = 3;  // K/V stages and P tiles, as the packed kernel
+constexpr int PA_N = 64;                    // keys per tile
+constexpr uint32_t PA_BLK = PA_N * 128;     // one 64-column block of a tile
+constexpr uint32_t PA_VST = 4 * PA_BLK;     // the blocks that are also V
+constexpr uint32_t PA_QBLK = 128 * 128;     // one 64-column block of Q
+constexpr int PA_NST = 3;                   // stages of the V blocks
+constexpr int PA_THREADS = 640;
+constexpr int PA_EPI0 = 8, PA_PROD0 = 12, PA_PRODUCERS = 7, PA_MMA = 19;
+constexpr int PA_SCAN_ROUNDS = 2048 / 32 / 4;  // index words per epilogue warp
+constexpr int PA_GRPS = (16 + PA_PRODUCERS - 1) / PA_PRODUCERS;                // groups of 4 keys per producer warp
+constexpr uint32_t PA_TM_O = 0, PA_TM_S = 256, PA_TM_Q = 320;
 
 // One work item's rows and its part of their keys.
 struct PaItem {
@@ -36,32 +67,56 @@ struct PaItem {
     bool ok;
 };
 
-struct PaLayout : AtLayout<PA_NST, false, PA_NPB, 1> {
-    using Base = AtLayout<PA_NST, false, PA_NPB, 1>;
-    static_assert(Base::EPI_STAGE && Base::EPI_COLS == 32, "the epilogue stages 32 columns of 32 rows");
-    static constexpr uint32_t OFF_ITEM = Base::SMEM;        // [2] PaItem
-    static constexpr uint32_t OFF_TMX = OFF_ITEM + 128;     // [2][128] the peer's true maxima
-    static constexpr uint32_t SMEM = OFF_TMX + 1024;
+struct PaLayout {
+    static constexpr uint32_t OFF_K = 0;
+    static constexpr uint32_t OFF_V = OFF_K + 5 * PA_BLK;
+    static constexpr uint32_t OFF_Q = OFF_V + PA_NST * PA_VST;   // three blocks of Q
+    static constexpr uint32_t OFF_P = OFF_Q + 3 * PA_QBLK;       // probabilities, no-swizzle K-major
+    static constexpr uint32_t OFF_EPI = OFF_P + 128 * PA_N * 2;  // per epilogue warp 32 rows x 128 bytes
+    static constexpr uint32_t OFF_ML = OFF_EPI + 4 * 4096;       // [2] maxima [128], sums [2][128]
+    static constexpr uint32_t OFF_XM = OFF_ML + 2 * 1536;        // [2][2][128] the key halves' maxima of a tile
+    static constexpr uint32_t OFF_VM = OFF_XM + 2 * 1024;        // [2][64] validity bits of 2048 slots
+    static constexpr uint32_t OFF_ITEM = OFF_VM + 512;           // [2] PaItem
+    static constexpr uint32_t OFF_INFO = OFF_ITEM + 128;         // [2][8] last used slot per epilogue warp
+    static constexpr uint32_t OFF_BAR = OFF_INFO + 64;
+    static constexpr uint32_t SMEM = OFF_BAR + 256;
 };
 static_assert(2 * sizeof(PaItem) <= 128, "item ring");
 static_assert(PaLayout::SMEM <= 232448, "shared memory budget");
 
-struct PaBars : AtBars {
-    uint64_t tm_full[8];  // [quadrant][2]: the peer's true maxima (bytes)
+struct PaBars {
+    uint64_t kfull[2], kfree[2];               // the two groups of the blocks that only S reads
+    uint64_t vfull[PA_NST], vfree[PA_NST];
+    uint64_t s_full, s_free;    // S complete / read by the softmax warps
+    uint64_t p_full, p_free;    // P written (and O rescaled) / its PV complete
+    uint64_t q_full, q_free;    // Q in place / its last S complete
+    uint64_t o_full, o_free;    // O complete / read by the epilogue
+    uint64_t xm_full[4];        // a tile's maxima of both key halves, per lane quadrant
+    uint64_t ml_full;           // an item's maxima and sums
+    uint64_t info_full[2], info_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
 };
-static_assert(sizeof(PaBars) <= 512, "barrier block");
+static_assert(sizeof(PaBars) <= 256, "barrier block");
 
-// 16 bytes global -> shared, or zeros (the source is then not read)
-DSA_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool have) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"((uint64_t)src), "r"(have ? 16 : 0)
-                 : "memory");
+DSA_DEV uint32_t pa_swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+
+// One lane of a converged warp.  Issuing tcgen05.mma under it, and not under
+// lane == 0, keeps the descriptors in uniform registers (32 against 45 cycles an
+// MMA of N 64).
+DSA_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred P; elect.sync _|P, 0xffffffff; selp.u32 %0, 1, 0, P; }" : "=r"(p));
+    return p != 0;
+}
+
+// 16 bytes global -> shared; n = 0: zeros, the source is not read
+DSA_DEV void cp_async16_n(uint32_t dst, const void* src, uint32_t n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"((uint64_t)src), "r"(n) : "memory");
 }
 
 DSA_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-
-DSA_DEV int32_t page_slot(const PageView& pv, int32_t s) {
-    return pv.shift >= 0 ? s & (pv.page_size - 1) : (int32_t)((uint32_t)s % (uint32_t)pv.page_size);
-}
 
 // First item slot of sequence b's groups: groups of R tokens never cross a
 // sequence; ceil(l / R) of them fit between floor(cu[b] / R) + b and the next.
@@ -101,7 +156,7 @@ DSA_DEV PaItem pa_item(const PagedAttnArgs& a, int64_t grp, int part, int sel_pa
     if (!it.ok || it.ntok == 0) return it;
     if (DENSE) {
         const int64_t n = it.pos0 + it.ntok;  // keys of the last row
-        const int64_t per = ((n + AT_N - 1) / AT_N + a.splits - 1) / a.splits * AT_N;
+        const int64_t per = ((n + PA_N - 1) / PA_N + a.splits - 1) / a.splits * PA_N;
         const int64_t lo = part * per;
         it.lo = (int)min(lo, n);
         it.count = (int)(min(n, lo + per) - it.lo);
@@ -113,724 +168,375 @@ DSA_DEV PaItem pa_item(const PagedAttnArgs& a, int64_t grp, int part, int sel_pa
 }
 
 template <bool DENSE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(AT_THREADS, 1)
-    attn_paged_kernel(const __grid_constant__ PagedAttnArgs a) {
-    static_assert(AT_SOFT0 % 4 == 0 && AT_PRODUCERS < AT_SOFT0, "warp roles");
-    constexpr int NST = PA_NST, NPB = PA_NPB;
+__global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_constant__ PagedAttnArgs a) {
     using Lay = PaLayout;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     PaBars* bars = (PaBars*)(smem + Lay::OFF_BAR);
     uint32_t* vmask = (uint32_t*)(smem + Lay::OFF_VM);
-    int* pmax = (int*)(smem + Lay::OFF_INFO);  // [2][8]
-    int* ntab = pmax + 16;                      // [AT_NTAB]
     PaItem* items = (PaItem*)(smem + Lay::OFF_ITEM);  // [2]
-    if ((uintptr_t)smem != (uintptr_t)smem_raw) {  // the layout needs a 1024-byte aligned base
+    int* pmax = (int*)(smem + Lay::OFF_INFO);         // [2][8]
+    if (smem_u32(smem) & 1023) {                      // the layout needs a 1024-byte aligned base
         if (threadIdx.x == 0) report(a.st, DSA_ERR_UNSUPPORTED, -3);
         return;
     }
-    const uint32_t warp = warp_id(), lane = lane_id();
-    const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
+    // (broadcasts tell the compiler that a value, and with it a branch or a loop, is
+    // the same in all lanes: only then do the MMA operands live in uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, (int)warp_id(), 0), lane = (int)lane_id();
     StatusHdr* st = a.st;
     volatile int* abort = &bars->abort;
 
-    // work items of this pair: pair + i * npairs
-    const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1, n_items = a.groups * a.splits;
-    const int64_t nq = pair < n_items ? (n_items - pair + npairs - 1) / npairs : 0;
-    const float scale_log2 = a.scale * 1.4426950408889634f;
-    // tiles of a selection's part (dense: from the item's own length)
-    const int sel_part = DENSE ? 0 : ((a.k_sel + AT_N - 1) / AT_N + a.splits - 1) / a.splits * AT_N;
-    const int nb = rank ? 5 : 4;      // 64-column blocks of K held here
-    const int col0 = rank ? 256 : 0;  // first K column
-    const int dv0 = rank ? 256 : 0;   // first output column
+    // this CTA's units: blockIdx.x + i * gridDim.x (an even grid: always the same half)
+    const int half = (int)(blockIdx.x & 1);
+    const int64_t item0 = blockIdx.x >> 1, step = gridDim.x >> 1, n_items = a.groups * a.splits;
+    const int64_t nq = item0 < n_items ? (n_items - item0 + step - 1) / step : 0;
+    // slots of a selection's part
+    const int sel_part = DENSE ? 0 : ((a.k_sel + PA_N - 1) / PA_N + a.splits - 1) / a.splits * PA_N;
+    // 64-column blocks of the row: V's four, and the other five (the first three of
+    // these have their Q in shared memory)
+    auto vblk = [&](int i) { return 4 * half + i; };
+    auto kblk = [&](int i) { return i == 4 ? 8 : 4 * (half ^ 1) + i; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NST; ++i) {
-            mbar_init(smem_u32(&bars->full[i]), AT_PRODUCERS * 32);
-            mbar_init(smem_u32(&bars->empty[i]), 1);
-        }
-        mbar_init(smem_u32(&bars->s_full), 2);   // one commit per issuer
-        mbar_init(smem_u32(&bars->s_empty), 8);  // 4 A + 4 B warps read every S tile
-        mbar_init(smem_u32(&bars->s_go), 1);
-        mbar_init(smem_u32(&bars->drain2), 1);
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(smem_u32(&bars->p_full[i]), 4);   // (only NPB of them are used)
-            mbar_init(smem_u32(&bars->p_free[i]), 2);
-        }
-        for (int i = 0; i < 8; ++i) {
-            mbar_init(smem_u32(&bars->tm_full[i]), 1);
-            mbar_arrive_expect_tx(smem_u32(&bars->tm_full[i]), 128);
-        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars->sx_full[i]), 1);
-            mbar_init(smem_u32(&bars->sx_free[i]), 4);
-            mbar_init(smem_u32(&bars->info_full[i]), AT_PRODUCERS);
-            mbar_init(smem_u32(&bars->info_empty[i]), 9);
+            mbar_init(smem_u32(&bars->kfull[i]), PA_PRODUCERS * 32);
+            mbar_init(smem_u32(&bars->kfree[i]), 1);
         }
+        for (int i = 0; i < PA_NST; ++i) {
+            mbar_init(smem_u32(&bars->vfull[i]), PA_PRODUCERS * 32);
+            mbar_init(smem_u32(&bars->vfree[i]), 1);
+        }
+        mbar_init(smem_u32(&bars->s_full), 1);
+        mbar_init(smem_u32(&bars->s_free), 8);
+        mbar_init(smem_u32(&bars->p_full), 8);
+        mbar_init(smem_u32(&bars->p_free), 1);
         mbar_init(smem_u32(&bars->q_full), 4);
+        mbar_init(smem_u32(&bars->q_free), 1);
         mbar_init(smem_u32(&bars->o_full), 1);
-        mbar_init(smem_u32(&bars->o_free), 8);
-        mbar_init(smem_u32(&bars->lx_full), 1);
-        mbar_init(smem_u32(&bars->lx_loc), 4);
+        mbar_init(smem_u32(&bars->o_free), 4);
+        mbar_init(smem_u32(&bars->ml_full), 8);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->xm_full[i]), 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->info_full[i]), 4);
+            mbar_init(smem_u32(&bars->info_empty[i]), 9 + PA_PRODUCERS);  // 8 softmax warps, the MMA warp, the producers
+        }
         mbar_init(smem_u32(&bars->drain), 1);
-        // byte counts of the first phase of every peer-filled barrier; each
-        // later phase is armed once the one before it has completed
-        for (int i = 0; i < NPB; ++i) mbar_expect_tx(smem_u32(&bars->p_full[i]), AT_PX_BYTES);
-        mbar_arrive_expect_tx(smem_u32(&bars->sx_full[0]), AT_SX_BYTES);
-        mbar_arrive_expect_tx(smem_u32(&bars->lx_full), AT_LX_BYTES);
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == AT_MMA_WARP) tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    if (warp == PA_MMA) tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tc_fence_before();
-    cluster_sync();  // barriers of both CTAs initialised and armed
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-
-    const uint32_t s_stage0 = smem_u32(smem);
-    const uint32_t s_p0 = smem_u32(smem + Lay::OFF_P);
-    const uint32_t s_qr = smem_u32(smem + Lay::OFF_QR);
-    // Half hf of the S tile of stage s: K-blocks 2hf, 2hf+1 (Q from TMEM) and, on
-    // rank 1, K-steps 2hf, 2hf+1 of the rope block (Q from shared memory), into
-    // accumulator hf.  Issued by one thread.
-    auto s_half = [&](int hf, uint32_t s) {
-        constexpr uint32_t idesc_s = idesc_make(1, 1, false, 128, AT_N);
-        const uint32_t kst = s_stage0 + s * Lay::STAGE;
-        const uint32_t d = tmem + TM_S + 64 * hf;
+    const uint32_t s_k = smem_u32(smem + Lay::OFF_K), s_v = smem_u32(smem + Lay::OFF_V);
+    // tiles of the item in ring slot qi & 1 (its info has arrived)
+    auto tiles_of = [&](int64_t qi) {
+        int mx = -1;
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-            const int kb = 2 * hf + k2;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_ts(d, tmem + TM_Q + kb * 32 + ks * 8, sdesc_sw128(kst + kb * AT_BLK + ks * 32, 16, 1024), idesc_s,
-                            (k2 | ks) ? 1u : 0u);
-        }
-        if (nb == 5)
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const int ks = 2 * hf + k2;
-                mma_bf16_ss(d, sdesc_sw128(s_qr + ks * 32, 16, 1024), sdesc_sw128(kst + 4 * AT_BLK + ks * 32, 16, 1024),
-                            idesc_s, 1u);
-            }
+        for (int w = 0; w < 4; ++w) mx = max(mx, pmax[(qi & 1) * 8 + w]);
+        return __shfl_sync(0xffffffffu, (mx + PA_N) / PA_N, 0);
     };
-    if (warp < AT_PRODUCERS) {
-        // ================= gather producers (6 warps) =================
-        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_WG0));
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_WG1));
-        // 16 groups of 4 keys per tile; warp w takes groups w, w+7, w+14
-        const int sub = (int)(lane >> 3), chunk = (int)(lane & 7);
-        const int ngrp = (16 - (int)warp + AT_PRODUCERS - 1) / AT_PRODUCERS;
-        uint32_t g = 0;  // tile of the pair's whole sequence
+    auto info_wait = [&](int64_t qi, int where) {
+        return wait_warp(smem_u32(&bars->info_full[qi & 1]), (uint32_t)((qi >> 1) & 1), abort, st, where);
+    };
+    auto info_done = [&](int64_t qi) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->info_empty[qi & 1]));
+    };
+
+    if (warp >= PA_PROD0 && warp < PA_MMA) {
+        // ================= gather producers =================
+        const int pw = warp - PA_PROD0;
+        // 16 groups of 4 keys per tile; warp w takes groups w, w + 7, w + 14
+        const int sub = lane >> 3, chunk = lane & 7;
+        const int ngrp = (16 - pw + PA_PRODUCERS - 1) / PA_PRODUCERS;
+        uint32_t g = 0;  // tile of the CTA's whole sequence
         bool ok = true;
-        const __nv_bfloat16* pool = (const __nv_bfloat16*)a.k + col0 + chunk * 8;
+        const __nv_bfloat16* pool = (const __nv_bfloat16*)a.k + chunk * 8;
         for (int64_t qi = 0; ok && qi < nq; ++qi) {
-            const uint32_t slot = (uint32_t)(qi & 1);
-            const int64_t item = pair + qi * npairs, grp = item / a.splits;
-            const PaItem it = pa_item<DENSE>(a, grp, (int)(item - grp * a.splits), sel_part);
+            if (!info_wait(qi, 0x2103)) break;
+            const PaItem it = items[qi & 1];
+            const int n_tiles = tiles_of(qi);
+            info_done(qi);
             const int32_t* irow = DENSE ? nullptr : a.idx + it.t0 * a.ld_idx + it.lo;
             const int count = it.count;  // keys (dense) or slots of this item's part
-            // ---- item info: rows, and for a selection the validity bits of its
-            // slots and the last used one ----
-            if (!wait_warp(smem_u32(&bars->info_empty[slot]), (uint32_t)((qi >> 1) & 1) ^ 1u, abort, st, 0x2102)) {
-                ok = false;
-                break;
-            }
-            int m = -1;
-            if constexpr (DENSE) {
-                m = count - 1;
-            } else {
-                int32_t v[AT_SCAN_ROUNDS];
-#pragma unroll
-                for (int r = 0; r < AT_SCAN_ROUNDS; ++r) {
-                    const int j = ((int)warp + AT_PRODUCERS * r) * 32 + (int)lane;
-                    v[r] = j < count ? __ldg(irow + j) : -1;
-                }
-#pragma unroll
-                for (int r = 0; r < AT_SCAN_ROUNDS; ++r) {
-                    const int w = (int)warp + AT_PRODUCERS * r;  // 32-slot word of the part
-                    bool val = v[r] >= 0;
-                    if (val && v[r] >= it.seqlen_k) {
-                        report(st, DSA_ERR_INDEX, it.t0);
-                        val = false;
-                    }
-                    if (val) {
-                        m = w * 32 + (int)lane;
-                        if (page_of(a.pv, it.b, v[r]).page < 0) {
-                            report(st, DSA_ERR_INDEX, it.t0);
-                            val = false;
-                        }
-                    }
-                    const uint32_t bits = __ballot_sync(0xffffffffu, val);
-                    if (lane == 0 && w < 64) vmask[slot * 64 + w] = bits;
-                }
-                for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            }
-            if (lane == 0) {
-                if (warp == 0) {
-                    items[slot] = it;
-                    if (!it.ok && rank == 0) report(st, DSA_ERR_INDEX, it.t0);
-                }
-                pmax[slot * 8 + warp] = m;
-                mbar_arrive(smem_u32(&bars->info_full[slot]));
-            }
-            if (!wait_warp(smem_u32(&bars->info_full[slot]), (uint32_t)((qi >> 1) & 1), abort, st, 0x2103)) {
-                ok = false;
-                break;
-            }
-            int mx = -1;
-#pragma unroll
-            for (int w = 0; w < AT_PRODUCERS; ++w) mx = max(mx, pmax[slot * 8 + w]);
-            const int n_tiles = (mx + AT_N) / AT_N;
-            // ---- pull the next item's Q rows (and its index row) into L2 while this
-            // item's tiles run ----
-            if (qi + 1 < nq) {
-                const int64_t gn = (item + npairs) / a.splits;
-                const PaItem nx = pa_item<DENSE>(a, gn, 0, sel_part);
-                if (!DENSE && warp == 0) {
-                    const char* ir = (const char*)(a.idx + nx.t0 * a.ld_idx);
-                    if (nx.ok)
-                        for (int off = (int)lane * 128; off < a.k_sel * 4; off += 32 * 128) prefetch_l2(ir + off);
-                } else if (warp >= 1 && warp <= 4) {
-                    const int row = (int)(warp - 1) * 32 + (int)lane;
-                    const int tk = row / a.heads;
-                    if (tk < nx.ntok) {
-                        const char* qr = (const char*)((const __nv_bfloat16*)a.q + (nx.t0 + tk) * a.q_stride_tok +
-                                                       (int64_t)(row - tk * a.heads) * a.q_stride_head + col0);
-                        for (int kb = 0; kb < nb; ++kb) prefetch_l2(qr + kb * 128);
-                    }
-                }
-            }
-            // ---- the item's tiles: position and page of this lane's rows, one tile ahead ----
-            int32_t nv[3] = {-1, -1, -1}, np[3] = {-1, -1, -1};
-            auto look_up = [&](int j) {
-#pragma unroll
-                for (int gi = 0; gi < 3; ++gi) {
-                    const int sj = j * AT_N + 4 * ((int)warp + AT_PRODUCERS * gi) + sub;
-                    nv[gi] = -1;
-                    if (gi < ngrp && sj < count) nv[gi] = DENSE ? it.lo + sj : __ldg(irow + sj);
-                    if (!DENSE && nv[gi] >= it.seqlen_k) nv[gi] = -1;
-                }
-#pragma unroll
-                for (int gi = 0; gi < 3; ++gi) np[gi] = nv[gi] >= 0 ? (int32_t)page_of(a.pv, it.b, nv[gi]).page : -1;
+            // ---- the item's tiles.  A row's place takes two dependent loads (its
+            // position, its page): positions are read two tiles ahead and pages one,
+            // so that neither is waited for. ----
+            auto position = [&](int j, int gi) -> int32_t {
+                const int sj = j * PA_N + 4 * (pw + PA_PRODUCERS * gi) + sub;
+                if (gi >= ngrp || sj >= count) return -1;
+                return DENSE ? it.lo + sj : __ldg(irow + sj);
             };
-            if (n_tiles > 0) look_up(0);
-            for (int j = 0; j < n_tiles; ++j, ++g) {
-                const uint32_t s = g % NST;
-                int32_t cv[3], cp[3];
+            const int32_t* table = a.pv.table + it.b * a.pv.ld_table;
+            int32_t np[PA_GRPS] = {}, ps[PA_GRPS], pg[PA_GRPS];  // positions of tile j + 1; slots and pages of tile j
+            auto look_up = [&](int gi) {
+                int32_t v = np[gi];
+                if (!DENSE && v >= it.seqlen_k) v = -1;
+                uint32_t p, o;
+                page_split(a.pv, (uint32_t)v, p, o);
+                ps[gi] = (int32_t)o;
+                pg[gi] = v >= 0 && (int64_t)p < a.pv.ld_table ? __ldg(table + p) : -1;
+            };
+            if (n_tiles > 0) {
 #pragma unroll
-                for (int gi = 0; gi < 3; ++gi) cv[gi] = nv[gi], cp[gi] = np[gi];
-                if (j + 1 < n_tiles) look_up(j + 1);
-                if (!wait_warp(smem_u32(&bars->empty[s]), ((g / NST) & 1) ^ 1, abort, st, 0x2101)) {
-                    ok = false;
-                    break;
+                for (int gi = 0; gi < PA_GRPS; ++gi) {
+                    np[gi] = position(0, gi);
+                    look_up(gi);
+                    np[gi] = position(1, gi);
                 }
-                const uint32_t kst = s_stage0 + s * Lay::STAGE;
+            }
+            for (int j = 0; j < n_tiles; ++j, ++g) {
+                const uint32_t s = g % PA_NST;
+                const __nv_bfloat16* src[PA_GRPS];
+                uint32_t n[PA_GRPS];
 #pragma unroll
-                for (int gi = 0; gi < 3; ++gi) {
-                    if (gi >= ngrp) break;
+                for (int gi = 0; gi < PA_GRPS; ++gi) {
                     // a slot that holds no row is filled with zeros, so that a masked
                     // probability of zero never meets a stray NaN or infinity
-                    const bool have = cp[gi] >= 0;
-                    if (DENSE && cv[gi] >= 0 && !have) report(st, DSA_ERR_INDEX, it.t0);
-                    const int32_t in = have ? page_slot(a.pv, cv[gi]) : 0;
-                    const int key = 4 * ((int)warp + AT_PRODUCERS * gi) + sub;  // key of the tile
-                    const __nv_bfloat16* src = have ? pool + (int64_t)cp[gi] * a.k_page_stride + (int64_t)in * a.k_stride : pool;
-                    const uint32_t dst = kst + swz(key, chunk);
-                    for (int kb = 0; kb < nb; ++kb) cp_async16_zfill(dst + kb * AT_BLK, have ? src + kb * 64 : src, have);
+                    const bool have = (uint32_t)pg[gi] < (uint32_t)a.pv.num_pages;
+                    if (DENSE && !have && gi < ngrp && j * PA_N + 4 * (pw + PA_PRODUCERS * gi) + sub < count)
+                        report(st, DSA_ERR_INDEX, it.t0);
+                    src[gi] = have ? pool + (int64_t)pg[gi] * a.k_page_stride + (int64_t)ps[gi] * a.k_stride : pool;
+                    n[gi] = have ? 16u : 0u;
+                    look_up(gi);
+                    np[gi] = position(j + 2, gi);
                 }
-                cp_async_arrive(smem_u32(&bars->full[s]));
+                bool got = true;
+                auto copy = [&](uint32_t base, int i0, int i1, bool v) {  // blocks [i0, i1) of this warp's rows
+#pragma unroll
+                    for (int gi = 0; gi < PA_GRPS; ++gi) {
+                        if (gi >= ngrp) break;
+                        const uint32_t dst = base + pa_swz(4 * (pw + PA_PRODUCERS * gi) + sub, chunk);
+#pragma unroll
+                        for (int i = i0; i < i1; ++i)
+                            cp_async16_n(dst + i * PA_BLK, src[gi] + (v ? vblk(i) : kblk(i)) * 64, n[gi]);
+                    }
+                };
+                got = wait_warp(smem_u32(&bars->kfree[0]), (g & 1) ^ 1, abort, st, 0x2101);
+                if (got) {
+                    copy(s_k, 0, 3, false);
+                    cp_async_arrive(smem_u32(&bars->kfull[0]));
+                    got = wait_warp(smem_u32(&bars->kfree[1]), (g & 1) ^ 1, abort, st, 0x2105);
+                }
+                if (got) {
+                    copy(s_k, 3, 5, false);
+                    cp_async_arrive(smem_u32(&bars->kfull[1]));
+                    got = wait_warp(smem_u32(&bars->vfree[s]), ((g / PA_NST) & 1) ^ 1, abort, st, 0x2104);
+                }
+                if (!got) { ok = false; break; }
+                copy(s_v + s * PA_VST, 0, 4, true);
+                cp_async_arrive(smem_u32(&bars->vfull[s]));
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == AT_MMA_WARP) {
+    } else if (warp == PA_MMA) {
         // ================= MMA issuer =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_WG1));
+        // The warp runs only a few MMAs ahead of the tensor core, so a wait, even for a
+        // barrier that is long complete, idles it unless long MMAs are queued.  Hence
+        // three waits a tile, the two that may be long behind the MMAs of PV and of
+        // group 0.  Operands are constants or uniform: the tensor memory is all this
+        // CTA's, so it begins at column 0, and the V stage is a template argument.
+        constexpr uint32_t idesc_s = idesc_make(1, 1, false, 128, PA_N);
         constexpr uint32_t idesc_pv = idesc_make(1, 1, true, 128, 256);
-        // Two cursors over the pair's tile sequence.  S cursor: query qs (ns
-        // tiles once its info is read, else -1), tile js, sequence tile gs,
-        // nqs queries with tiles begun.  PV cursor: query-with-tiles nqu, tile
-        // ju, sequence tile gu; tile counts of begun queries are kept in ntab.
-        int64_t qs = 0;
-        int js = 0, ns = -1, ju = 0;
-        uint32_t gs = 0, nqs = 0, gu = 0, nqu = 0;
-        bool ok = true;
-        long long idle0 = clock64();
-        while (ok && (qs < nq || nqu < nqs)) {
-            bool done = false;
-            // ---- PV cursor (S(gu) issued, so its query has begun) ----
-            if (gu < gs) {
-                const int nu = ntab[nqu % AT_NTAB];
-                const uint32_t b = gu % NPB;
-                bool rdy = mbar_probe(smem_u32(&bars->p_full[b]), (gu / NPB) & 1);
-                if (ju == 0 && nqu > 0) rdy = rdy && mbar_probe(smem_u32(&bars->o_free), (nqu - 1) & 1);
-                if (__all_sync(0xffffffffu, rdy)) {
-                    tc_fence_after();
-                    if (lane == 0) {
-                        mbar_expect_tx(smem_u32(&bars->p_full[b]), AT_PX_BYTES);  // its next phase
-                        const uint32_t vb = s_stage0 + (gu % NST) * Lay::STAGE;
-                        const uint32_t pb = s_p0 + b * AT_TILE128;
+        const uint32_t base = smem_u32(smem);
+        auto issue_sk = [&](auto grp_c) {  // S over group 0 (Q in shared memory) or 1 (in tensor memory)
+            constexpr int grp = decltype(grp_c)::value;
+            if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < AT_N / 16; ++ks)
-                            mma_bf16_ss(tmem + TM_O, sdesc_noswz(pb + ks * 4096, 2048, 128),
-                                        sdesc_sw128(vb + ks * 2048, AT_BLK, 1024), idesc_pv, (ju > 0 || ks > 0) ? 1u : 0u);
-                        mma_commit(smem_u32(&bars->empty[gu % NST]));
-                        mma_commit_mc(smem_u32(&bars->p_free[b]), (uint16_t)3);
-                        if (ju + 1 == nu) mma_commit(smem_u32(&bars->o_full));
-                    }
-                    __syncwarp();
-                    ++gu;
-                    if (++ju == nu) {
-                        ju = 0;
-                        ++nqu;
-                    }
-                    done = true;
-                }
-            }
-            // ---- S cursor ----
-            if (!done && qs < nq) {
-                if (ns < 0) {
-                    const uint32_t slot = (uint32_t)(qs & 1);
-                    if (__all_sync(0xffffffffu, mbar_probe(smem_u32(&bars->info_full[slot]), (uint32_t)((qs >> 1) & 1)))) {
-                        int mx = -1;
+                for (int i = grp ? 3 : 0; i < (grp ? 5 : 3); ++i)
 #pragma unroll
-                        for (int w = 0; w < AT_PRODUCERS; ++w) mx = max(mx, pmax[slot * 8 + w]);
-                        ns = (mx + AT_N) / AT_N;
-                        if (lane == 0) {
-                            if (ns > 0) ntab[nqs % AT_NTAB] = ns;
-                            mbar_arrive(smem_u32(&bars->info_empty[slot]));
-                        }
-                        __syncwarp();
-                        if (ns == 0) {
-                            ns = -1;
-                            ++qs;
-                        }
-                        done = true;
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t kd = sdesc_sw128(base + Lay::OFF_K + i * PA_BLK + ks * 32, 16, 1024);
+                        if (grp == 0)
+                            mma_bf16_ss(PA_TM_S, sdesc_sw128(base + Lay::OFF_Q + i * PA_QBLK + ks * 32, 16, 1024), kd, idesc_s,
+                                        (i | ks) ? 1u : 0u);
+                        else
+                            mma_bf16_ts(PA_TM_S, PA_TM_Q + (i - 3) * 32 + ks * 8, kd, idesc_s, 1u);
                     }
-                } else {
-                    const uint32_t s = gs % NST;
-                    bool rdy = mbar_probe(smem_u32(&bars->full[s]), (gs / NST) & 1) &&
-                               mbar_probe(smem_u32(&bars->s_empty), (gs & 1) ^ 1);
-                    if (js == 0) rdy = rdy && mbar_probe(smem_u32(&bars->q_full), nqs & 1);
-                    if (__all_sync(0xffffffffu, rdy)) {
-                        fence_proxy_async();
-                        tc_fence_after();
-                        if (lane == 0) {
-                            // first half of S: blocks 0, 1 (+ rope K-steps 0, 1); the
-                            // second issuer adds blocks 2, 3 (+ rope 2, 3) into its own
-                            // accumulator
-                            bars->go[gs & 1] = (int)s;
-                            mbar_arrive(smem_u32(&bars->s_go));
-                            s_half(0, s);
-                            mma_commit(smem_u32(&bars->s_full));
-                        }
-                        __syncwarp();
-                        ++gs;
-                        if (++js == ns) {
-                            js = 0;
-                            ns = -1;
-                            ++qs;
-                            ++nqs;
-                        }
-                        done = true;
-                    }
-                }
+                mma_commit(smem_u32(&bars->kfree[grp]));
             }
-            if (done) {
-                idle0 = clock64();
-            } else {
-                const long long el = clock64() - idle0;
-                bool give_up = *abort != 0;
-                if (!give_up && el > (1ll << 20) && *(volatile int*)&st->code == DSA_ERR_TIMEOUT) give_up = true;
-                if (!give_up && el > kWaitBudget) {
-                    report(st, DSA_ERR_TIMEOUT, 0x2203);
-                    give_up = true;
-                }
-                if (__any_sync(0xffffffffu, give_up)) {
-                    *abort = 1;
-                    ok = false;
-                }
-            }
-        }
-        if (ok && lane == 0) {  // no more S tiles
-            bars->go[gs & 1] = -1;
-            mbar_arrive(smem_u32(&bars->s_go));
-        }
-        if (*abort && lane == 0) {
-            mma_commit(smem_u32(&bars->drain));
-            mbar_wait(smem_u32(&bars->drain), 0, nullptr, st, 0x2205, 1ll << 28);
-        }
-    } else if (warp == AT_MMA2_WARP) {
-        // ================= second S issuer =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AT_REGS_WG1));
-        for (uint32_t g = 0;; ++g) {
-            if (!wait_warp(smem_u32(&bars->s_go), g & 1, abort, st, 0x2401)) break;
-            const int s = *(volatile int*)&bars->go[g & 1];
-            if (s < 0) break;
-            fence_proxy_async();
-            tc_fence_after();
-            if (lane == 0) {
-                s_half(1, (uint32_t)s);
+            __syncwarp();
+        };
+        auto issue_sv = [&](auto s_c, bool last) {
+            constexpr uint32_t vst = Lay::OFF_V + decltype(s_c)::value * PA_VST;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_ts(PA_TM_S, PA_TM_Q + (2 + i) * 32 + ks * 8,
+                                    sdesc_sw128(base + vst + i * PA_BLK + ks * 32, 16, 1024), idesc_s, 1u);
                 mma_commit(smem_u32(&bars->s_full));
+                if (last) mma_commit(smem_u32(&bars->q_free));
             }
             __syncwarp();
-        }
-        if (*abort && lane == 0) {
-            mma_commit(smem_u32(&bars->drain2));
-            mbar_wait(smem_u32(&bars->drain2), 0, nullptr, st, 0x2405, 1ll << 28);
-        }
-    } else {
-        // ================= softmax / exchange / epilogue (8 warps) =================
-        // Stage-specialised: warps 8..11 ("A", one per TMEM lane quadrant) read
-        // each S tile, form the row's partial maximum and send the peer's 32
-        // partial columns; warps 12..15 ("B") read their own 32 columns of the
-        // same tile, combine them with the peer's partials, form the
-        // probabilities and write P.  Both groups run every tile concurrently.
-        // Per query: load Q (after the previous query's last S), finish the
-        // previous query (row sums, O / l), then the tiles.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AT_REGS_SOFT));
-        const uint32_t quad = warp & 3;
-        const bool is_b = warp >= AT_SOFT0 + 4;
-        const int h = (int)(quad * 32 + lane);
-        const uint32_t lane_off = (quad * 32) << 16;
-        const int kh = (int)rank;  // this CTA's key half of every tile
-        uint8_t* sx = smem + Lay::OFF_SX;
-        const int tok_off = h / a.heads, head = h - tok_off * a.heads;  // this row's token of the item, and head
-        const float* pmx = (const float*)(smem + Lay::OFF_PM);
-        float* tmx = (float*)(smem + Lay::OFF_TMX);  // [2][128] the peer's true maxima
-        const uint32_t peer_tmx = mapa(smem_u32(tmx), peer);
-        const uint32_t peer_tm_full0 = mapa(smem_u32(&bars->tm_full[0]), peer);
-        uint32_t n_tm = 0;  // exchanges of true maxima so far
-        float* lx = (float*)(smem + Lay::OFF_LX);
-        const float* lxr = (const float*)(smem + Lay::OFF_LXR);
-        const uint32_t peer_sx = mapa(smem_u32(sx), peer);
-        const uint32_t peer_pm = mapa(smem_u32(smem + Lay::OFF_PM), peer);
-        const uint32_t peer_lxr = mapa(smem_u32(smem + Lay::OFF_LXR), peer);
-        const uint32_t peer_p = mapa(s_p0, peer);
-        const uint32_t peer_sx_full0 = mapa(smem_u32(&bars->sx_full[0]), peer);
-        const uint32_t peer_sx_free0 = mapa(smem_u32(&bars->sx_free[0]), peer);
-        const uint32_t peer_p_full0 = mapa(smem_u32(&bars->p_full[0]), peer);
-        const uint32_t peer_lx_full = mapa(smem_u32(&bars->lx_full), peer);
-        const uint32_t my_sx_full0 = smem_u32(&bars->sx_full[0]), my_sx_free0 = smem_u32(&bars->sx_free[0]);
-        const uint32_t my_p_full0 = smem_u32(&bars->p_full[0]), my_p_free0 = smem_u32(&bars->p_free[0]);
-        const bool arm_thread = threadIdx.x == (AT_SOFT0 + 4) * 32;
-        const int ocol = is_b ? 0 : 128;  // this warp's 128 of the CTA's 256 output columns
-
-        // The item's rows of the output.  One part: O / l in bf16 and the lse.
-        // Several: normalised fp32 partials and their base-2 lse, per item.
-        // Rows leave through this warp's staging tile, so that a store covers
-        // 64-byte pieces of 8 rows.
-        uint8_t* stg = smem + Lay::OFF_EPI + (warp - AT_SOFT0) * Lay::EPI_WARP_BYTES;
-        auto write_lse = [&](const PaItem& it, int64_t item, float v) {  // base 2; -inf: nothing attended
-            if (rank != 0 || !is_b) return;
-            if (a.splits > 1) a.part_lse[item * 128 + h] = v;
-            else if (a.lse && tok_off < it.ntok) a.lse[(it.t0 + tok_off) * a.heads + head] = v * 0.69314718055994531f;
         };
-        // element offsets in the output of the rows 8 i + lane / 4 of this warp
-        // (-1: not a row of the item)
-        auto out_rows = [&](const PaItem& it, int64_t (&off)[4]) {
-            const int64_t mine = tok_off < it.ntok
-                                     ? (it.t0 + tok_off) * a.out_stride_tok + (int64_t)head * a.out_stride_head + dv0 + ocol
-                                     : -1;
+        auto issue_pv = [&](auto s_c, bool first, bool last) {
+            constexpr uint32_t s = decltype(s_c)::value, vst = Lay::OFF_V + s * PA_VST;
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, 8 * i + (int)(lane >> 2));
-        };
-        auto epilogue = [&](const PaItem& it, int64_t item, uint32_t e, float m_used, float l) -> bool {
-            float l_tot = 0.f;
-            if (is_b) {
-                // the peer's buffer is free: it read its previous sums before its
-                // A warps sent the partials of this item's tiles
-                st_async_b32(peer_lxr + h * 4, __float_as_uint(l), peer_lx_full);
-                if (!wait_warp(smem_u32(&bars->lx_full), e & 1, abort, st, 0x2308)) return false;
-                l_tot = l + lxr[h];
-                if (arm_thread) mbar_arrive_expect_tx(smem_u32(&bars->lx_full), AT_LX_BYTES);  // its next phase
-                lx[h] = l_tot;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->lx_loc));
-            } else {
-                if (!wait_warp(smem_u32(&bars->lx_loc), e & 1, abort, st, 0x2306)) return false;
-                l_tot = lx[h];
+                for (int ks = 0; ks < PA_N / 16; ++ks)
+                    mma_bf16_ss(PA_TM_O, sdesc_noswz(base + Lay::OFF_P + ks * 4096, 2048, 128),
+                                sdesc_sw128(base + vst + ks * 2048, PA_BLK, 1024), idesc_pv, (!first || ks > 0) ? 1u : 0u);
+                mma_commit(smem_u32(&bars->vfree[s]));
+                mma_commit(smem_u32(&bars->p_free));
+                if (last) mma_commit(smem_u32(&bars->o_full));
             }
-            if (!wait_warp(smem_u32(&bars->o_full), e & 1, abort, st, 0x2309)) return false;
+            __syncwarp();
+        };
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
+        using C2 = std::integral_constant<int, 2>;
+        static_assert(PA_NST == 3, "three V stages below");
+        // two barriers in one wait: even lanes poll the first, odd lanes the second
+        auto wait2 = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, int where) {
+            const bool got = wait_warp(smem_u32((lane & 1) ? b1 : b0), (lane & 1) ? p1 : p0, abort, st, where);
+            __syncwarp();
             tc_fence_after();
-            const float inv = l_tot != 0.f ? 1.0f / l_tot : 0.f;  // a NaN sum stays a NaN row
-            uint32_t r[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_off + TM_O + ocol + c * 32, r[c]);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));  // O may be overwritten now
-            write_lse(it, item, l_tot != 0.f ? m_used + __log2f(l_tot) : -INFINITY);
-            if (a.splits > 1) {
-                float* base = a.part_o + (item * 128 + quad * 32) * 512 + dv0 + ocol;
-#pragma unroll
-                for (int qc = 0; qc < 8; ++qc) {  // 16 columns at a time
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t* x = &r[qc >> 1][16 * (qc & 1) + 4 * k];
-                        *(float4*)(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
-                            make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
-                                        __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 8 * i + (int)(lane >> 2), k = (int)(lane & 3);
-                        *(float4*)(base + (int64_t)row * 512 + qc * 16 + k * 4) =
-                            *(const float4*)(stg + row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
-                    }
-                    __syncwarp();
-                }
-                return true;
-            }
-            int64_t off[4];
-            out_rows(it, off);
-            __nv_bfloat16* out = (__nv_bfloat16*)a.out;
-#pragma unroll
-            for (int qc = 0; qc < 4; ++qc) {  // 32 columns at a time
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        w[p] = pack_bf16(__uint_as_float(r[qc][8 * k + 2 * p]) * inv,
-                                         __uint_as_float(r[qc][8 * k + 2 * p + 1]) * inv);
-                    *(uint4*)(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 8 * i + (int)(lane >> 2), k = (int)(lane & 3);
-                    const uint4 v = *(const uint4*)(stg + row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
-                    if (off[i] >= 0) *(uint4*)(out + off[i] + qc * 32 + k * 8) = v;
-                }
-                __syncwarp();
-            }
+            return got;
+        };
+        uint32_t g = 0, e = 0;  // tiles and items (with tiles) begun
+        bool ok = true, pend = false, pend_first = false, pend_last = false;  // PV(g - 1) is still to be issued
+        auto pv = [&]() -> bool {
+            const uint32_t p = g - 1, s = p % PA_NST;
+            // a first tile overwrites O: the epilogue of the item before (of those
+            // begun, the one before the pending tile's) has read it
+            const bool o_read = pend_first && e > 1;
+            if (!wait2(&bars->p_full, p & 1, o_read ? &bars->o_free : &bars->p_full, o_read ? (e & 1) : (p & 1), 0x2201))
+                return false;
+            if (s == 0) issue_pv(C0(), pend_first, pend_last);
+            else if (s == 1) issue_pv(C1(), pend_first, pend_last);
+            else issue_pv(C2(), pend_first, pend_last);
+            pend = false;
             return true;
         };
-
-        uint32_t g = 0;    // tile of the pair's whole sequence
-        uint32_t nqt = 0;  // items with tiles begun
-        bool ok = true;
-        bool pend = false;  // an item's epilogue is still to be done
-        int64_t item_pend = 0;
-        PaItem it_pend = {};
-        float m_pend = -INFINITY, l_pend = 0.f;
         for (int64_t qi = 0; ok && qi < nq; ++qi) {
-            const int64_t item = pair + qi * npairs;
-            const uint32_t slot = (uint32_t)(qi & 1);
-            if (!wait_warp(smem_u32(&bars->info_full[slot]), (uint32_t)((qi >> 1) & 1), abort, st, 0x2310)) {
-                ok = false;
-                break;
-            }
-            const PaItem it = items[slot];
-            int mx = -1;
-#pragma unroll
-            for (int w = 0; w < AT_PRODUCERS; ++w) mx = max(mx, pmax[slot * 8 + w]);
-            const int n_tiles = (mx + AT_N) / AT_N;
-            if (n_tiles == 0) {  // nothing to attend to: zero rows, lse -inf (a part: its lse alone)
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->info_empty[slot]));
-                write_lse(it, item, -INFINITY);
-                if (a.splits == 1 && tok_off < it.ntok) {
-                    uint4* dst = (uint4*)((__nv_bfloat16*)a.out + (it.t0 + tok_off) * a.out_stride_tok +
-                                          (int64_t)head * a.out_stride_head + dv0 + ocol);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                continue;
-            }
-            // ---- Q of this item -> TMEM (A operand of S = Q K^T), by the A warps,
-            // which finish an item's tiles first; every S of the earlier items has
-            // completed (this warp saw its s_full).  Rows past the item are zero. ----
-            if (!is_b) {
-                const bool row_ok = tok_off < it.ntok;
-                const __nv_bfloat16* qrow = (const __nv_bfloat16*)a.q +
-                                            (row_ok ? (it.t0 + tok_off) * a.q_stride_tok + (int64_t)head * a.q_stride_head : 0) +
-                                            col0;
-                uint4 qreg[5][8];
-#pragma unroll
-                for (int kb = 0; kb < 5; ++kb) {
-                    if (kb < nb) {
-                        const uint4* src = (const uint4*)(qrow + kb * 64);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) qreg[kb][j] = row_ok ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-#pragma unroll
-                for (int kb = 0; kb < 5; ++kb) {
-                    if (kb >= nb) continue;
-                    uint32_t r[32];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        r[4 * j] = qreg[kb][j].x;
-                        r[4 * j + 1] = qreg[kb][j].y;
-                        r[4 * j + 2] = qreg[kb][j].z;
-                        r[4 * j + 3] = qreg[kb][j].w;
-                    }
-                    if (kb < 4) {
-                        tmem_st32(tmem + lane_off + TM_Q + kb * 32, r);
-                    } else {
-                        uint8_t* qr = smem + Lay::OFF_QR;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            *(uint4*)(qr + swz(h, c)) = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
-                    }
-                }
-                tmem_wait_st();
+            if (!info_wait(qi, 0x2203)) { ok = false; break; }
+            const int n_tiles = tiles_of(qi);
+            info_done(qi);
+            if (n_tiles == 0) continue;
+            if (!wait_warp(smem_u32(&bars->q_full), e & 1, abort, st, 0x2204)) { ok = false; break; }
+            ++e;
+            for (int u = 0; u < n_tiles; ++u) {
+                const uint32_t s = g % PA_NST;
+                if (!wait2(&bars->s_free, (g & 1) ^ 1, &bars->kfull[0], g & 1, 0x2205)) { ok = false; break; }
+                fence_proxy_async();  // the rows arrived by cp.async (P's writers fence their own)
+                issue_sk(C0());
+                if (!wait2(&bars->kfull[1], g & 1, &bars->vfull[s], (g / PA_NST) & 1, 0x2206)) { ok = false; break; }
                 fence_proxy_async();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+                issue_sk(C1());
+                const bool last = u + 1 == n_tiles;
+                if (s == 0) issue_sv(C0(), last);
+                else if (s == 1) issue_sv(C1(), last);
+                else issue_sv(C2(), last);
+                if (pend && !pv()) { ok = false; break; }
+                pend = true;
+                pend_first = u == 0;
+                pend_last = last;
+                ++g;
             }
-            // ---- the previous item's epilogue (this item's first S overlap it) ----
-            if (pend) {
-                if (!epilogue(it_pend, item_pend, nqt - 1, m_pend, l_pend)) {
-                    ok = false;
-                    break;
-                }
-                pend = false;
+            // the item's last PV, before anything of the next is waited for
+            if (ok && pend) ok = pv();
+        }
+        if (*abort) {
+            if (elect_one()) {
+                mma_commit(smem_u32(&bars->drain));
+                mbar_wait(smem_u32(&bars->drain), 0, nullptr, st, 0x2208, 1ll << 28);
             }
-            // keys of the part that this row may see (dense)
-            const int lim = DENSE ? (int)min((int64_t)it.count, max((int64_t)0, it.pos0 + tok_off + 1 - it.lo)) : 0;
+            __syncwarp();
+        }
+    } else if (warp < PA_EPI0) {
+        // ================= softmax: two threads per row, 32 keys of a tile each =================
+        const int quad = warp & 3, kh = warp >> 2, h = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const float scale_log2 = a.scale * 1.4426950408889634f;
+        const bool zero = scale_log2 == 0.f;
+        const int tok_off = h / a.heads;  // this row's token of the item
+        uint8_t* prow = smem + Lay::OFF_P + kh * 4 * 2048 + h * 16;
+        float* xm = (float*)(smem + Lay::OFF_XM);
+        uint32_t g = 0, e = 0;
+        bool ok = true;
+        for (int64_t qi = 0; ok && qi < nq; ++qi) {
+            if (!info_wait(qi, 0x2301)) break;
+            const int n_tiles = tiles_of(qi);
+            // keys of the part that this row may see (dense), from this half's first
+            int lim = 0;
+            if constexpr (DENSE) {
+                const PaItem& it = items[qi & 1];
+                lim = (int)min((int64_t)it.count, max((int64_t)0, it.pos0 + tok_off + 1 - it.lo)) - 32 * kh;
+            }
+            const uint32_t* vm = vmask + (qi & 1) * 64 + kh;
             float m_used = -INFINITY, l = 0.f;
-            for (int u = 0; ok && u < n_tiles; ++u, ++g) {
-                constexpr uint32_t xb = 0;
-                const uint32_t xph = g & 1;  // phase of the partial-score buffer
-                uint32_t mlo, mhi;           // keys of the tile that this row sees
-                if constexpr (DENSE) {
-                    const int n = min(max(lim - u * AT_N, 0), AT_N);
-                    mlo = low_bits(n);
-                    mhi = low_bits(n - 32);
-                } else {
-                    mlo = vmask[slot * 64 + 2 * u];
-                    mhi = vmask[slot * 64 + 2 * u + 1];
-                }
-                if (!wait_warp(smem_u32(&bars->s_full), g & 1, abort, st, 0x2301)) { ok = false; break; }
+            for (int u = 0; u < n_tiles; ++u, ++g) {
+                const uint32_t msk = DENSE ? low_bits(lim - u * PA_N) : vm[2 * u];  // keys that this row sees
+                if (!wait_warp(smem_u32(&bars->s_full), g & 1, abort, st, 0x2302)) { ok = false; break; }
                 tc_fence_after();
-                // this CTA's partial S = accumulator 0 + accumulator 1, both key
-                // halves read in one TMEM round trip; stage A sends the peer's
-                // half on before it forms the partial maximum
-                const uint32_t ta = tmem + lane_off + TM_S;
-                const int ph_ = kh ^ 1, oh = kh;  // key halves: the peer's, this CTA's
-                uint32_t rp[32], ro[32], xo[32];
-                {
-                    uint32_t x[32];
-                    tmem_ld32(ta + 32 * ph_, rp);
-                    tmem_ld32(ta + 64 + 32 * ph_, x);
-                    tmem_ld32(ta + 32 * oh, ro);
-                    tmem_ld32(ta + 64 + 32 * oh, xo);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) rp[i] = __float_as_uint(__uint_as_float(rp[i]) + __uint_as_float(x[i]));
-                }
-                if (!is_b) {
-                    // ---- stage A: send the peer's 32 partial columns, then the partial max ----
-                    if (!wait_warp(my_sx_free0 + 8 * xb, xph ^ 1, abort, st, 0x2302)) { ok = false; break; }
-                    const uint32_t dst = peer_sx + xb * AT_TILE128;
-                    const uint32_t bar = peer_sx_full0 + 8 * xb;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        st_async_v4(dst + chunk_off(h, c), rp[4 * c], rp[4 * c + 1], rp[4 * c + 2], rp[4 * c + 3], bar);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) ro[i] = __float_as_uint(__uint_as_float(ro[i]) + __uint_as_float(xo[i]));
+                uint32_t x[32];
+                tmem_ld32(tmem + lane_off + PA_TM_S + 32 * kh, x);
+                tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty));
-                const uint32_t mo = kh ? mhi : mlo, mp = kh ? mlo : mhi;  // valid slots of the own / peer half
-                float pm = -INFINITY;  // partial maximum of this CTA's row over the tile's valid keys
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if ((mo >> i) & 1u) pm = fmaxf(pm, __uint_as_float(ro[i]));
-                    if ((mp >> i) & 1u) pm = fmaxf(pm, __uint_as_float(rp[i]));
-                }
-                if (!is_b) {
-                    st_async_b32(peer_pm + xb * 512 + h * 4, __float_as_uint(pm), peer_sx_full0 + 8 * xb);
-                    continue;
-                }
-                // ---- stage B: combine, probabilities, both copies of P ----
-                const uint32_t msk = mo;
-                if (!wait_warp(my_sx_full0 + 8 * xb, xph, abort, st, 0x2303)) { ok = false; break; }
-                if (arm_thread) mbar_arrive_expect_tx(my_sx_full0 + 8 * xb, AT_SX_BYTES);  // its next phase
-                float s32[32];
-                {
-                    const uint8_t* rowp = sx + xb * AT_TILE128;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 v = *(const float4*)(rowp + chunk_off(h, c));
-                        const float pv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s32[4 * c + e] = __uint_as_float(ro[4 * c + e]) + pv[e];
-                    }
-                }
-                const float pm_peer = pmx[xb * 128 + h];
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(peer_sx_free0 + 8 * xb);
-                // The sum of the two partial maxima bounds every score of the row, and
-                // both CTAs form it alike.  While it stays within 2^8 of the running
-                // maximum, that maximum serves.  Where it does not, the warps of these
-                // heads in both CTAs exchange the true maxima of their keys: the bound
-                // alone may lie so far above the scores that all of exp underflows.
-                const float mb = (pm == -INFINITY || pm_peer == -INFINITY) ? -INFINITY : (pm + pm_peer) * scale_log2;
-                float alpha = 1.f;
-                if (__any_sync(0xffffffffu, !(mb <= m_used + 8.0f))) {
-                    float tm = -INFINITY;
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
+                if (__any_sync(0xffffffffu, msk != 0xffffffffu)) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if ((msk >> i) & 1u) tm = fmaxf(tm, s32[i]);
-                    const uint32_t tb = n_tm & 1;
-                    st_async_b32(peer_tmx + tb * 512 + h * 4, __float_as_uint(tm), peer_tm_full0 + 8 * (quad * 2 + tb));
-                    const uint32_t bar = smem_u32(&bars->tm_full[quad * 2 + tb]);
-                    if (!wait_warp(bar, (n_tm >> 1) & 1, abort, st, 0x2307)) { ok = false; break; }
-                    const float mt = fmaxf(tm, tmx[tb * 128 + h]) * scale_log2;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(bar, 128);  // its next phase
-                    ++n_tm;
-                    if (mt > m_used + 8.0f) {
-                        alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mt);
-                        l *= alpha;
-                        m_used = mt;
-                    }
+                        if (!((msk >> i) & 1u)) x[i] = 0xff800000u;  // -inf
                 }
-                uint32_t pw[16];
-                {
-                    // (scores of -inf alone: probabilities of 0, not of exp2(-inf + inf))
-                    const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-                    float rs0 = 0.f, rs1 = 0.f;
+                float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = ((msk >> (2 * i)) & 1u) ? ex2(fmaf(s32[2 * i], scale_log2, -m_sub)) : 0.f;
-                        const float p1 = ((msk >> (2 * i + 1)) & 1u) ? ex2(fmaf(s32[2 * i + 1], scale_log2, -m_sub)) : 0.f;
-                        rs0 += p0;
-                        rs1 += p1;
-                        pw[i] = pack_bf16(p0, p1);
-                    }
-                    l += rs0 + rs1;
+                for (int i = 0; i < 32; ++i) mt[i & 3] = fmaxf(mt[i & 3], __uint_as_float(x[i]));
+                float mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+                {  // with the other half's
+                    float* slot = xm + (g & 1) * 256;
+                    slot[kh * 128 + h] = mx;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->xm_full[quad]));
+                    if (!wait_warp(smem_u32(&bars->xm_full[quad]), g & 1, abort, st, 0x2303)) { ok = false; break; }
+                    mx = fmaxf(mx, slot[(kh ^ 1) * 128 + h]);
                 }
-                // P tile pb is free once PV(g - NPB) is done in both CTAs
-                const uint32_t pb = g % NPB;
-                if (!wait_warp(my_p_free0 + 8 * pb, ((g / NPB) & 1) ^ 1, abort, st, 0x2304)) { ok = false; break; }
-                {
-                    uint8_t* prow = smem + Lay::OFF_P + pb * AT_TILE128;
-                    const uint32_t pdst = peer_p + pb * AT_TILE128;
-                    const uint32_t bar = peer_p_full0 + 8 * pb;
+                // (no key seen: -inf, also where scale is 0)
+                const float ms = mx == -INFINITY ? -INFINITY : mx * scale_log2;
+                // the running maximum moves only when it grows by more than 2^8
+                float alpha = 1.f;
+                if (ms > m_used + 8.0f) {
+                    alpha = m_used == -INFINITY ? 0.f : ex2(m_used - ms);
+                    l *= alpha;
+                    m_used = ms;
+                }
+                // the probabilities; rounding them to bf16 for the MMA is half a step
+                // (2^-8) of each, their sum is kept unrounded in fp32.  A masked key is
+                // -inf here, unless scale is 0 (-inf * 0): its probability is set apart.
+                const float sub = m_used == -INFINITY ? 0.f : m_used;
+                float rs[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t w[16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int c = 4 * kh + q;
-                        *(uint4*)(prow + chunk_off(h, c)) = make_uint4(pw[4 * q], pw[4 * q + 1], pw[4 * q + 2], pw[4 * q + 3]);
-                        st_async_v4(pdst + chunk_off(h, c), pw[4 * q], pw[4 * q + 1], pw[4 * q + 2], pw[4 * q + 3], bar);
+                        const int i = 8 * c + 2 * q;
+                        float p0 = ex2(fmaf(__uint_as_float(x[i]), scale_log2, -sub));
+                        float p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale_log2, -sub));
+                        if (zero) {
+                            p0 = ((msk >> i) & 1u) ? p0 : 0.f;
+                            p1 = ((msk >> (i + 1)) & 1u) ? p1 : 0.f;
+                        }
+                        rs[q & 1] += p0;
+                        rs[2 + (q & 1)] += p1;
+                        w[4 * c + q] = pack_bf16(p0, p1);
                     }
                 }
-                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // O may be rescaled only between PV(g-1) and PV(g)
-                    const uint32_t w = g - 1;
-                    if (!wait_warp(my_p_free0 + 8 * (w % NPB), (w / NPB) & 1, abort, st, 0x2305)) { ok = false; break; }
+                l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                // P may be written, and O rescaled, once PV(g - 1) is complete
+                if (!wait_warp(smem_u32(&bars->p_free), (g & 1) ^ 1, abort, st, 0x2304)) { ok = false; break; }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *(uint4*)(prow + c * 2048) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // each half takes 128 of the columns
                     tc_fence_after();
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         uint32_t r[32];
-                        const uint32_t ta = tmem + lane_off + TM_O + c * 32;
+                        const uint32_t ta = tmem + lane_off + PA_TM_O + kh * 128 + c * 32;
                         tmem_ld32(ta, r);
                         tmem_wait_ld();
 #pragma unroll
@@ -842,25 +548,242 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(AT_THREADS, 1)
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(my_p_full0 + 8 * pb);
+                if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
             }
             if (!ok) break;
+            info_done(qi);
+            if (n_tiles == 0) continue;
+            float* ml = (float*)(smem + Lay::OFF_ML) + (e & 1) * 384;
+            if (kh == 0) ml[h] = m_used;
+            ml[128 + kh * 128 + h] = l;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->info_empty[slot]));
-            pend = true;
-            it_pend = it;
-            item_pend = item;
-            m_pend = m_used;
-            l_pend = l;
-            ++nqt;
+            if (lane == 0) mbar_arrive(smem_u32(&bars->ml_full));
+            ++e;
         }
-        if (ok && pend) ok = epilogue(it_pend, item_pend, nqt - 1, m_pend, l_pend);
+    } else {
+        // ================= Q loads and the epilogue: one thread per row =================
+        const int quad = warp - PA_EPI0, h = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const int tok_off = h / a.heads, head = h - tok_off * a.heads;
+        const int dv0 = 256 * half;
+        uint8_t* stg = smem + Lay::OFF_EPI + quad * 4096;
+        // base 2; -inf: nothing attended
+        auto write_lse = [&](const PaItem& it, int64_t item, float v) {
+            if (half != 0) return;
+            if (a.splits > 1) a.part_lse[item * 128 + h] = v;
+            else if (a.lse && tok_off < it.ntok) a.lse[(it.t0 + tok_off) * a.heads + head] = v * 0.69314718055994531f;
+        };
+        // The item's rows of the output.  One part: O / l in bf16 and the lse.
+        // Several: normalised fp32 partials and their base-2 lse, per item.
+        // Rows leave through this warp's staging tile, so that a store covers
+        // 64-byte pieces of 8 rows.
+        auto epilogue = [&](const PaItem& it, int64_t item, uint32_t e) -> bool {
+            if (!wait_warp(smem_u32(&bars->ml_full), e & 1, abort, st, 0x2401)) return false;
+            const float* ml = (const float*)(smem + Lay::OFF_ML) + (e & 1) * 384;
+            const float m_used = ml[h], l = ml[128 + h] + ml[256 + h];
+            const float inv = l != 0.f ? 1.0f / l : 0.f;  // a NaN sum stays a NaN row
+            if (!wait_warp(smem_u32(&bars->o_full), e & 1, abort, st, 0x2402)) return false;
+            tc_fence_after();
+            const int64_t mine = tok_off < it.ntok
+                                     ? (it.t0 + tok_off) * a.out_stride_tok + (int64_t)head * a.out_stride_head + dv0
+                                     : -1;
+            int64_t off[4];  // output rows 8 i + lane / 4 of this warp (-1: not a row of the item)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2));
+            __nv_bfloat16* out = (__nv_bfloat16*)a.out;
+            float* part = a.part_o + (item * 128 + quad * 32) * 512 + dv0;
+            const int k4 = lane & 3;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {  // 32 columns at a time
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_off + PA_TM_O + c * 32, r);
+                tmem_wait_ld();
+                if (c == 7) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));  // O may be overwritten now
+                }
+                if (a.splits > 1) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {  // 16 columns at a time
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t* x = &r[16 * q + 4 * k];
+                            *(float4*)(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                                make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
+                                            __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 8 * i + (lane >> 2);
+                            *(float4*)(part + (int64_t)row * 512 + c * 32 + q * 16 + k4 * 4) =
+                                *(const float4*)(stg + row * 64 + ((k4 ^ ((row >> 1) & 3)) << 4));
+                        }
+                        __syncwarp();
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            w[p] = pack_bf16(__uint_as_float(r[8 * k + 2 * p]) * inv, __uint_as_float(r[8 * k + 2 * p + 1]) * inv);
+                        *(uint4*)(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 8 * i + (lane >> 2);
+                        const uint4 v = *(const uint4*)(stg + row * 64 + ((k4 ^ ((row >> 1) & 3)) << 4));
+                        if (off[i] >= 0) *(uint4*)(out + off[i] + c * 32 + k4 * 8) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+            write_lse(it, item, l != 0.f ? m_used + __log2f(l) : -INFINITY);
+            return true;
+        };
+
+        // Item qi's rows, and for a selection the validity bits of its slots and the
+        // last used one, one item ahead of the other warps.
+        auto publish = [&](int64_t qi) -> bool {
+            const uint32_t slot = (uint32_t)(qi & 1);
+            const int64_t item = item0 + qi * step, grp = item / a.splits;
+            const PaItem it = pa_item<DENSE>(a, grp, (int)(item - grp * a.splits), sel_part);
+            // Q rows into L2 (their loads begin when the item before has issued its last S)
+            if (tok_off < it.ntok) {
+                const char* qr = (const char*)((const __nv_bfloat16*)a.q + (it.t0 + tok_off) * a.q_stride_tok +
+                                               (int64_t)head * a.q_stride_head);
+                for (int kb = 0; kb < 9; ++kb) prefetch_l2(qr + kb * 128);
+            }
+            if (!wait_warp(smem_u32(&bars->info_empty[slot]), (uint32_t)((qi >> 1) & 1) ^ 1u, abort, st, 0x2102)) return false;
+            int m = -1;
+            if constexpr (DENSE) {
+                m = it.count - 1;
+            } else {
+                const int32_t* irow = a.idx + it.t0 * a.ld_idx + it.lo;
+                int32_t v[PA_SCAN_ROUNDS];
+#pragma unroll
+                for (int r = 0; r < PA_SCAN_ROUNDS; ++r) {
+                    const int j = (quad + 4 * r) * 32 + lane;
+                    v[r] = j < it.count ? __ldg(irow + j) : -1;
+                }
+#pragma unroll
+                for (int r = 0; r < PA_SCAN_ROUNDS; ++r) {
+                    const int w = quad + 4 * r;  // 32-slot word of the part
+                    bool val = v[r] >= 0;
+                    if (val) m = w * 32 + lane;
+                    if (val && (v[r] >= it.seqlen_k || page_of(a.pv, it.b, v[r]).page < 0)) {
+                        report(st, DSA_ERR_INDEX, it.t0);
+                        val = false;
+                    }
+                    const uint32_t bits = __ballot_sync(0xffffffffu, val);
+                    if (lane == 0) vmask[slot * 64 + w] = bits;
+                }
+                for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
+            if (lane == 0) {
+                if (quad == 0) {
+                    items[slot] = it;
+                    if (!it.ok && half == 0) report(st, DSA_ERR_INDEX, it.t0);
+                }
+                pmax[slot * 8 + quad] = m;
+                mbar_arrive(smem_u32(&bars->info_full[slot]));
+            }
+            __syncwarp();
+            return true;
+        };
+        // Q of an item: three blocks into shared memory, six through registers and
+        // this warp's staging tile (a row a lane) into tensor memory.  Rows past the
+        // item are zero.  Loads take 4 rows x 128 bytes an instruction: a row a lane
+        // costs 32 cache lines each (9200 cycles an item, now about 2500).
+        auto load_q = [&](const PaItem& it, uint32_t e) -> bool {
+            const int sub = lane >> 3, chunk = lane & 7;
+            int64_t off[8];  // rows 4 j + sub of this warp
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = quad * 32 + 4 * j + sub, tk = r / a.heads;
+                off[j] = tk < it.ntok ? (it.t0 + tk) * a.q_stride_tok + (int64_t)(r - tk * a.heads) * a.q_stride_head + chunk * 8
+                                      : -1;
+            }
+            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
+            uint4 x[8];
+            auto fetch = [&](int blk) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = off[j] >= 0 ? __ldg((const uint4*)(q + off[j] + blk * 64)) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            auto blk_of = [&](int i) { return i < 2 ? kblk(3 + i) : vblk(i - 2); };  // tensor-memory blocks in their order
+            fetch(blk_of(0));
+            if (e > 0 && !wait_warp(smem_u32(&bars->q_free), (e - 1) & 1, abort, st, 0x2404)) return false;
+            tc_fence_after();
+            const uint32_t sq = smem_u32(smem + Lay::OFF_Q);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    cp_async16_n(sq + i * PA_QBLK + pa_swz(quad * 32 + 4 * j + sub, chunk),
+                                 q + (off[j] >= 0 ? off[j] + kblk(i) * 64 : 0), off[j] >= 0 ? 16u : 0u);
+#pragma unroll 1
+            for (int i = 0; i < 6; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *(uint4*)(stg + pa_swz(4 * j + sub, chunk)) = x[j];
+                __syncwarp();
+                if (i < 5) fetch(blk_of(i + 1));
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 v = *(const uint4*)(stg + pa_swz(lane, c));
+                    r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+                }
+                tmem_st32(tmem + lane_off + PA_TM_Q + i * 32, r);
+                __syncwarp();
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tmem_wait_st();
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+            return true;
+        };
+
+        uint32_t e = 0;     // items with tiles begun
+        bool ok = nq == 0 || publish(0), pend = false;  // the (e - 1)-th item's epilogue is still to be done
+        int64_t item_pend = 0;
+        PaItem it_pend = {};
+        for (int64_t qi = 0; ok && qi < nq; ++qi) {
+            const int64_t item = item0 + qi * step;
+            if (!info_wait(qi, 0x2403)) { ok = false; break; }
+            const PaItem it = items[qi & 1];
+            const int n_tiles = tiles_of(qi);
+            if (n_tiles > 0 && !load_q(it, e)) { ok = false; break; }
+            // ---- the previous item's epilogue (this item's first S overlaps it) ----
+            if (pend && !epilogue(it_pend, item_pend, e - 1)) { ok = false; break; }
+            pend = false;
+            if (n_tiles == 0) {  // nothing to attend to: zero rows, lse -inf (a part: its lse alone)
+                write_lse(it, item, -INFINITY);
+                if (a.splits == 1 && tok_off < it.ntok) {
+                    uint4* dst = (uint4*)((__nv_bfloat16*)a.out + (it.t0 + tok_off) * a.out_stride_tok +
+                                          (int64_t)head * a.out_stride_head + dv0);
+#pragma unroll 4
+                    for (int i = 0; i < 32; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else {
+                pend = true;
+                it_pend = it;
+                item_pend = item;
+                ++e;
+            }
+            if (qi + 1 < nq && !publish(qi + 1)) { ok = false; break; }
+        }
+        if (ok && pend) epilogue(it_pend, item_pend, e - 1);
     }
     tc_fence_before();
-    __syncwarp();
-    cluster_sync();  // no DSMEM traffic may target a CTA that has exited
+    __syncthreads();
     tc_fence_after();
-    if (warp == AT_MMA_WARP) tmem_dealloc(tmem, 512);
+    if (warp == PA_MMA) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of every item's rows: weights 2^(lse_p - max), one block a
@@ -873,18 +796,29 @@ __global__ void __launch_bounds__(128) attn_paged_combine_kernel(const PagedAttn
     if (tok >= it.ntok) return;
     const int64_t t = it.t0 + tok;
     const float* pl = a.part_lse + grp * a.splits * 128 + row;
-    float m = -INFINITY;
-    for (int p = 0; p < a.splits; ++p) m = fmaxf(m, __ldg(pl + p * 128));
+    grid_wait();
+    // lane p of every warp holds the weights of parts p and p + 32
+    const int lane = (int)lane_id();
+    float m = -INFINITY, z[2], w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        z[i] = lane + 32 * i < a.splits ? pl[(lane + 32 * i) * 128] : -INFINITY;
+        m = fmaxf(m, z[i]);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = z[i] == -INFINITY ? 0.f : ex2(z[i] - m);  // NaN stays NaN
     const float* po = a.part_o + (grp * a.splits * 128 + row) * 512 + threadIdx.x * 4;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
+#pragma unroll 4
     for (int p = 0; p < a.splits; ++p) {
-        const float z = __ldg(pl + p * 128);
-        if (z == -INFINITY) continue;  // an empty part: its rows were not written
-        const float w = ex2(z - m);    // NaN stays NaN
-        const float4 v = __ldg((const float4*)(po + (int64_t)p * 128 * 512));
-        l += w;
-        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+        const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
+        if (wp == 0.f) continue;  // an empty part: its rows were not written
+        const float4 v = *(const float4*)(po + (int64_t)p * 128 * 512);
+        l += wp;
+        o.x = fmaf(wp, v.x, o.x), o.y = fmaf(wp, v.y, o.y), o.z = fmaf(wp, v.z, o.z), o.w = fmaf(wp, v.w, o.w);
     }
     const float inv = l != 0.f ? 1.0f / l : 0.f;
     *(uint2*)((__nv_bfloat16*)a.out + t * a.out_stride_tok + (int64_t)head * a.out_stride_head + threadIdx.x * 4) =
@@ -893,50 +827,21 @@ __global__ void __launch_bounds__(128) attn_paged_combine_kernel(const PagedAttn
         a.lse[t * a.heads + head] = l != 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// CTA pairs that can be resident at once (the persistent grid).
-template <bool DENSE>
-static int pa_pairs_resident() {
-    static int cached = 0;
-    if (cached > 0) return cached;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * 1024, 1, 1);
-    cfg.blockDim = dim3(AT_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = PaLayout::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, (const void*)attn_paged_kernel<DENSE>, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        n = 0;
-    }
-    if (n > 0) cached = n;
-    return n;
-}
-
 template <bool DENSE>
 static bool pa_launch(const PagedAttnArgs& a, cudaStream_t s) {
-    const void* fn = (const void*)attn_paged_kernel<DENSE>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PaLayout::SMEM) != cudaSuccess) return false;
-    // the setmaxnreg split must fit the registers the block is launched with
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess || (int64_t)fa.numRegs * AT_THREADS < (int64_t)AT_REGS_SPLIT)
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return false;
-    const int pairs = pa_pairs_resident<DENSE>();
-    if (pairs <= 0) return false;
-    const int64_t items = a.groups * a.splits;
-    const int64_t grid = items < pairs ? items : pairs;
-    attn_paged_kernel<DENSE><<<(unsigned)(2 * grid), AT_THREADS, PaLayout::SMEM, s>>>(a);
+    if (cudaFuncSetAttribute((const void*)attn_paged_kernel<DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PaLayout::SMEM) != cudaSuccess)
+        return false;
+    const int64_t units = 2 * a.groups * a.splits, most = sms & ~1;
+    attn_paged_kernel<DENSE><<<(unsigned)(units < most ? units : most), PA_THREADS, PaLayout::SMEM, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return false;
-    if (a.splits > 1) {
-        const int64_t rows = a.groups * a.group * a.heads;
-        attn_paged_combine_kernel<<<(unsigned)rows, 128, 0, s>>>(a, DENSE ? 1 : 0);
-    }
-    return cudaGetLastError() == cudaSuccess;
+    if (a.splits == 1) return true;
+    return launch_after(attn_paged_combine_kernel, dim3((unsigned)(a.groups * a.group * a.heads)), dim3(128), s, a,
+                        DENSE ? 1 : 0);
 }
 
 bool launch_paged_attn_tc(const PagedAttnArgs& a, cudaStream_t s) {

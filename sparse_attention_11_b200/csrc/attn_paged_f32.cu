@@ -189,18 +189,29 @@ __global__ void __launch_bounds__(128) attn_paged_f32_combine_kernel(const Paged
     const int64_t t = blockIdx.x;
     const int lane = (int)lane_id();
     if (!row_info(a.sv, t).ok) return;  // left as it was
+    grid_wait();
     for (int h = (int)warp_id(); h < a.heads; h += 4) {
-        float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < a.splits; ++p) m = fmaxf(m, a.part_lse[(t * a.splits + p) * a.heads + h]);
+        // lane p holds the weights of parts p and p + 32
+        float z[2], m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int p = lane + 32 * i;
+            z[i] = p < a.splits ? a.part_lse[(t * a.splits + p) * a.heads + h] : -INFINITY;
+            m = fmaxf(m, z[i]);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        float w[2], l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = z[i] == -INFINITY ? 0.f : expf(z[i] - m);  // an empty part; NaN stays NaN
+#pragma unroll 4
         for (int p = 0; p < a.splits; ++p) {
+            const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
             const int64_t r = (t * a.splits + p) * a.heads + h;
-            const float z = a.part_lse[r];
-            if (z == -INFINITY) continue;
-            const float w = expf(z - m);
-            l += w;
+            l += wp;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (lane + 32 * x < a.dv) o[x] = fmaf(w, a.part_o[r * a.dv + lane + 32 * x], o[x]);
+                if (lane + 32 * x < a.dv) o[x] = fmaf(wp, a.part_o[r * a.dv + lane + 32 * x], o[x]);
         }
         const float inv = l != 0.f ? 1.0f / l : 0.f;
         float* op = (float*)a.out + t * a.out_stride_tok + h * a.out_stride_head;
@@ -224,8 +235,7 @@ static bool pf_launch(const PagedAttnArgs& a, cudaStream_t s) {
         return false;
     attn_paged_f32_kernel<DK, DV><<<(unsigned)grid, PF_WARPS * 32, smem, s>>>(a, vec);
     if (cudaGetLastError() != cudaSuccess) return false;
-    if (a.splits > 1) attn_paged_f32_combine_kernel<<<(unsigned)a.total_q, 128, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess;
+    return a.splits == 1 || launch_after(attn_paged_f32_combine_kernel, dim3((unsigned)a.total_q), dim3(128), s, a);
 }
 
 template <int DK>

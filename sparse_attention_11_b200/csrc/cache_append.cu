@@ -3,7 +3,8 @@
 // to the pool's type) and the indexer key (norm, rotation, and for an FP8 pool
 // the e4m3 codes with one fp32 scale per token, amax / 448).
 //
-// One warp per token and part, the row in registers; bound by launch latency
+// One warp per token, its row and key in registers (a warp for each of the two
+// looks the position up twice: 14.6 us for 9500 tokens); bound by launch latency
 // for a decode step (a few hundred KB) and by HBM for a prefill chunk.
 //
 // The indexer key is computed in 64 bits.  Its codes are a rounding to 4
@@ -39,13 +40,12 @@ DSA_DEV uint32_t e4m3_of(double q) {
 }
 
 // The indexer key of one token by one warp: lane l holds columns 4l..4l+3.
-template <class T>
-DSA_DEV void append_key(const AppendArgs& a, const T* __restrict__ x, const float* __restrict__ cs, const PageRef& pr,
-                        int lane, double* sm) {
+DSA_DEV void append_key(const AppendArgs& a, const float (&x)[4], const float* __restrict__ cs, const PageRef& pr, int lane,
+                        double* sm) {
     const RowXform& ra = a.idx_row;
     double v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (double)load1(x + 4 * lane + e);
+    for (int e = 0; e < 4; ++e) v[e] = (double)x[e];
     if (ra.norm_dim > 0) {
         double ss = 0.0;
 #pragma unroll
@@ -96,36 +96,46 @@ template <class T, int NC>
 __global__ void __launch_bounds__(AP_WARPS * 32) cache_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) uint8_t ap_sm[];
     const int lane = (int)lane_id(), warp = (int)warp_id();
-    const int64_t u = (int64_t)blockIdx.x * AP_WARPS + warp;
-    const int64_t t = u / a.parts;
+    const int64_t t = (int64_t)blockIdx.x * AP_WARPS + warp;
     if (t >= a.total_q) return;
-    const bool key = a.parts == 2 ? (u & 1) : a.kv == nullptr;  // parts: KV row, indexer key
-    const RowXform& ra = key ? a.idx_row : a.kv_row;
+    // the token's row first: its place takes three or more dependent loads
+    const T* x = (const T*)a.kv_new + t * a.kv_new_stride;
+    Raw8<T> row[NC > 0 ? NC : 1];
+    float kx[4];
+    if (a.idx_new) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kx[e] = load1((const T*)a.idx_new + t * a.idx_new_stride + 4 * lane + e);
+    }
+    if constexpr (NC > 0) load_row<T, 32, NC>(row, x, a.dim, lane, a.kv_new != nullptr);
     const RowInfo ri = row_info(a.sv, t);
     PageRef pr;
     pr.page = -1;
     pr.slot = 0;
-    const bool ok = ri.ok && (ra.rope_dim == 0 || ri.pos < ra.rope_positions);
+    // (a table that a part without rotation does not read has no end)
+    bool ok = ri.ok;
+    if (a.kv_new && a.kv_row.rope_dim) ok = ok && ri.pos < a.kv_row.rope_positions;
+    if (a.idx_new && a.idx_row.rope_dim) ok = ok && ri.pos < a.idx_row.rope_positions;
     if (ok) pr = page_of(a.pv, ri.b, ri.pos);
     if (!ok || pr.page < 0) {
         if (lane == 0) report(a.st, DSA_ERR_INDEX, t);
         return;
     }
-    const float* cs = ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr;
+    auto angles = [&](const RowXform& ra) { return ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr; };
     uint8_t* sm = ap_sm + warp * a.warp_smem;
-    if (key) {
-        append_key<T>(a, (const T*)a.idx_new + t * a.idx_new_stride, cs, pr, lane, (double*)sm);
-        return;
-    }
-    const T* x = (const T*)a.kv_new + t * a.kv_new_stride;
+    if (a.idx_new) append_key(a, kx, angles(a.idx_row), pr, lane, (double*)sm);
+    if (!a.kv_new) return;
+    __syncwarp();
+    const RowXform& ra = a.kv_row;
+    const float* cs = angles(ra);
     T* y = (T*)a.kv + pr.page * a.kv_page_stride + (int64_t)pr.slot * a.kv_stride;
-    if constexpr (NC > 0) row_forward<T, 32, NC>(x, y, ra, a.dim, cs, lane, true, (float*)sm);
-    else row_forward_scalar<T>(x, y, ra, a.dim, cs, lane);
+    if constexpr (NC > 0) {
+        row_forward<T, 32, NC>(row, y, ra, a.dim, cs, lane, true, (float*)sm);
+    } else row_forward_scalar<T>(x, y, ra, a.dim, cs, lane);
 }
 
 template <class T, int NC>
 static bool ap_launch(const AppendArgs& a, cudaStream_t s) {
-    const int64_t blocks = (a.total_q * a.parts + AP_WARPS - 1) / AP_WARPS;
+    const int64_t blocks = (a.total_q + AP_WARPS - 1) / AP_WARPS;
     if (blocks >= ((int64_t)1 << 31)) return false;
     cache_append_kernel<T, NC><<<(unsigned)blocks, AP_WARPS * 32, AP_WARPS * a.warp_smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess;

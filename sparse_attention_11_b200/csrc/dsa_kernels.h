@@ -241,7 +241,7 @@ struct RowXform {
     int64_t rope_positions;
 };
 constexpr int kRowMaxDim = 2048;
-constexpr int kNormRopeBwdBlocks = 148 * 4;
+constexpr int kNormRopeBwdBlocks = 148 * 2;  // as many as are resident
 
 struct NormRopeArgs {
     SeqView sv;
@@ -266,7 +266,6 @@ struct AppendArgs {
     SeqView sv;
     PageView pv;
     int64_t total_q;
-    int parts;             // 1 or 2: KV row and / or indexer key
     int dim;               // columns of a KV row
     const void* kv_new;
     int64_t kv_new_stride;

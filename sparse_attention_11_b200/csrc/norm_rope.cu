@@ -41,28 +41,52 @@ DSA_DEV void token_pos(TokenPos& tp, int64_t t, const SeqView& sv, const RowXfor
     tp.cs = tp.ok && ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr;
 }
 
+// A lane group's walk over rows: token and head follow by addition (a 64-bit
+// division a row costs more than the row's arithmetic).
+struct RowWalk {
+    int64_t r, t;
+    int h;
+};
+DSA_DEV RowWalk walk_from(int64_t r, int heads) {
+    RowWalk w;
+    w.r = r;
+    w.t = r / heads;
+    w.h = (int)(r - w.t * heads);
+    return w;
+}
+DSA_DEV void walk_on(RowWalk& w, int n, int heads) {
+    w.r += n;
+    if (heads == 1) {
+        w.t += n;
+        return;
+    }
+    w.h += n;
+    while (w.h >= heads) w.h -= heads, ++w.t;
+}
+
 template <class T, int G, int NC>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 4 : 1) norm_rope_kernel(const NormRopeArgs a) {
     extern __shared__ __align__(16) float nr_sm[];
     constexpr int RPW = 32 / G;  // rows per warp and step
     const int lane = (int)lane_id(), gl = lane % G, sub = lane / G, warp = (int)warp_id();
     float* sm = nr_sm + (warp * RPW + sub) * a.ra.rope_dim;
     const int64_t rows = a.total_q * a.heads;
-    int64_t r = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp + sub;
-    const int64_t r_end = min(rows, r - sub + a.rows_per_warp);
+    const int64_t r0 = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp;
+    const int64_t r_end = min(rows, r0 + a.rows_per_warp);
+    RowWalk w = walk_from(r0 + sub, a.heads);
     TokenPos tp;
-    for (int64_t r0 = r - sub; r0 < r_end; r0 += RPW, r += RPW) {
-        bool live = r < r_end;
-        const T* x = nullptr;
-        T* y = nullptr;
+    // One row at a time: many small warps hide the loads better than rows in flight
+    // (a row ahead: 120 registers, 565 us for 8192 x 128 x 576 in bf16).
+    for (int64_t rr = r0; rr < r_end; rr += RPW) {
+        bool live = w.r < r_end;
+        Raw8<T> cur[NC];
+        load_row<T, G, NC>(cur, (const T*)a.x + w.t * a.x_stride_tok + w.h * a.x_stride_head, a.dim, gl, live);
         if (live) {
-            const int64_t t = r / a.heads, h = r - t * a.heads;
-            token_pos(tp, t, a.sv, a.ra, a.st);
+            token_pos(tp, w.t, a.sv, a.ra, a.st);
             live = tp.ok;
-            x = (const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head;
-            y = (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head;
         }
-        row_forward<T, G, NC>(x, y, a.ra, a.dim, tp.cs, gl, live, sm);
+        row_forward<T, G, NC>(cur, (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head, a.ra, a.dim, tp.cs, gl, live, sm);
+        walk_on(w, RPW, a.heads);
     }
 }
 
@@ -84,7 +108,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_scalar_kernel(const Norm
 // Backward
 // ---------------------------------------------------------------------------
 template <class T, int G, int NC>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_kernel(const NormRopeArgs a) {
     extern __shared__ __align__(16) float nr_sm[];
     constexpr int RPW = 32 / G;
     const int lane = (int)lane_id(), gl = lane % G, sub = lane / G, warp = (int)warp_id();
@@ -96,74 +120,85 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_kernel(const NormRop
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
-    int64_t r = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp + sub;
-    const int64_t r_end = min(rows, r - sub + a.rows_per_warp);
-    TokenPos tp;
-    for (int64_t r0 = r - sub; r0 < r_end; r0 += RPW, r += RPW) {
-        bool live = r < r_end;
-        const T *x = nullptr, *dy = nullptr;
-        T* dx = nullptr;
-        if (live) {
-            const int64_t t = r / a.heads, h = r - t * a.heads;
-            token_pos(tp, t, a.sv, a.ra, a.st);
-            live = tp.ok;
-            x = (const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head;
-            dy = (const T*)a.dy + t * a.dy_stride_tok + h * a.dy_stride_head;
-            dx = (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head;
-        }
-        float g[NC][8], xv[NC][8];
+    const int64_t r0 = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp;
+    const int64_t r_end = min(rows, r0 + a.rows_per_warp);
+    RowWalk w = walk_from(r0 + sub, a.heads);
+    auto fetch = [&](const RowWalk& k, Raw8<T>(&rx)[NC], Raw8<T>(&rg)[NC]) {
+        load_row<T, G, NC>(rg, (const T*)a.dy + k.t * a.dy_stride_tok + k.h * a.dy_stride_head, a.dim, gl, k.r < r_end);
+        load_row<T, G, NC>(rx, (const T*)a.x + k.t * a.x_stride_tok + k.h * a.x_stride_head, n, gl, k.r < r_end);
+    };
+    // the next row is in flight while this one is worked on, where registers allow
+    constexpr bool AHEAD = NC * (int)sizeof(T) <= 8;
+    // the weight stays in registers where they allow
+    constexpr bool KEEP_W = NC <= 2;
+    float wt[KEEP_W ? NC : 1][8];
+    if (KEEP_W)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
+        for (int i = 0; i < (KEEP_W ? NC : 1); ++i) {
             const int c = (gl + G * i) * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = 0.f, xv[i][e] = 0.f;
-            if (live && c < a.dim) load8(dy + c, g[i]);
-            if (live && c < n) load8(x + c, xv[i]);
+            for (int x = 0; x < 8; ++x) wt[i][x] = 1.f;
+            if (a.ra.weight && c < n) load_weight8(a.ra.weight, c, wt[i]);
         }
+    Raw8<T> cx[NC], cg[NC];
+    if (AHEAD) fetch(w, cx, cg);
+    TokenPos tp;
+    for (int64_t rr = r0; rr < r_end; rr += RPW) {
+        RowWalk nw = w;
+        walk_on(nw, RPW, a.heads);
+        Raw8<T> nx[NC], ng[NC];
+        if (AHEAD) fetch(nw, nx, ng);
+        else fetch(w, cx, cg);
+        bool live = w.r < r_end;
+        if (live) {
+            token_pos(tp, w.t, a.sv, a.ra, a.st);
+            live = tp.ok;
+        }
+        T* dx = (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head;
+        float g[NC][8], xv[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) unpack8(cg[i], g[i]), unpack8(cx[i], xv[i]);
         if (a.ra.rope_dim > 0) rotate_chunks<G, NC>(g, a.ra, tp.cs, gl, -1.f, live, sm);
         if (n > 0) {
             float ss = 0.f, dot = 0.f;
-            float w[NC][8];
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if ((gl + G * i) * 8 < n)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(xv[i][e], xv[i][e], ss);
+            ss = group_sum<G>(ss);
+            const float rstd = 1.0f / sqrtf(ss / (float)n + a.ra.eps);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (gl + G * i) * 8;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
                 if (c < n) {
-                    if (a.ra.weight) {
-                        const float4 p = __ldg((const float4*)(a.ra.weight + c));
-                        const float4 q = __ldg((const float4*)(a.ra.weight + c) + 1);
-                        w[i][0] = p.x, w[i][1] = p.y, w[i][2] = p.z, w[i][3] = p.w;
-                        w[i][4] = q.x, w[i][5] = q.y, w[i][6] = q.z, w[i][7] = q.w;
-                    }
+                    float(&wc)[8] = wt[KEEP_W ? i : 0];
+                    if (!KEEP_W && a.ra.weight) load_weight8(a.ra.weight, c, wc);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        ss = fmaf(xv[i][e], xv[i][e], ss);
-                        dot = fmaf(g[i][e] * w[i][e], xv[i][e], dot);
+                        xv[i][e] *= rstd;  // x^
+                        if (live) acc[i][e] = fmaf(g[i][e], xv[i][e], acc[i][e]);
+                        if (KEEP_W || a.ra.weight) g[i][e] *= wc[e];
+                        dot = fmaf(g[i][e], xv[i][e], dot);
                     }
                 }
             }
-            ss = group_sum<G>(ss);
-            dot = group_sum<G>(dot);
-            const float rstd = 1.0f / sqrtf(ss / (float)n + a.ra.eps);
-            const float k = dot * rstd / (float)n;  // mean of g w x^
+            const float k = group_sum<G>(dot) / (float)n;  // mean of g w x^
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                if ((gl + G * i) * 8 < n) {
+            for (int i = 0; i < NC; ++i)
+                if ((gl + G * i) * 8 < n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float xh = xv[i][e] * rstd;
-                        if (live) acc[i][e] = fmaf(g[i][e], xh, acc[i][e]);
-                        g[i][e] = rstd * (g[i][e] * w[i][e] - xh * k);
-                    }
-                }
-            }
+                    for (int e = 0; e < 8; ++e) g[i][e] = rstd * (g[i][e] - xv[i][e] * k);
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (gl + G * i) * 8;
             if (live && c < a.dim) store8(dx + c, g[i]);
         }
+        w = nw;
+        if (AHEAD)
+#pragma unroll
+            for (int i = 0; i < NC; ++i) cx[i] = nx[i], cg[i] = ng[i];
     }
     if (!a.dw_part) return;
     // the block's groups, added in order; each warp's RPW row groups first
@@ -252,13 +287,16 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const 
 
 // dw[c] = sum over the blocks' partial rows, in a fixed order: 32 strided sums
 // in 64 bits, then those in order.
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int blocks, int n,
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int blocks, int n,
                                                             float* __restrict__ dw) {
     __shared__ double sm[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     double v = 0.0;
-    if (c < n)
-        for (int b = threadIdx.y; b < blocks; b += 32) v += (double)__ldg(part + (int64_t)b * n + c);
+    grid_wait();
+    if (c < n) {
+#pragma unroll 5
+        for (int b = threadIdx.y; b < blocks; b += 32) v += (double)part[(int64_t)b * n + c];
+    }
     sm[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && c < n) {
@@ -275,7 +313,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
 template <class T, int G, int NC>
 static bool nr_launch(NormRopeArgs a, bool bwd, int blocks, cudaStream_t s) {
     const int groups = NR_THREADS / G;
-    size_t smem = a.ra.interleaved ? 0 : (size_t)groups * a.ra.rope_dim * 4;
+    const int d = rope_in_lane<G>(a.ra);
+    size_t smem = a.ra.interleaved || (d > 0 && d < NC && NC > 1) ? 0 : (size_t)groups * a.ra.rope_dim * 4;
     if (bwd && a.dw_part && smem < (size_t)NR_WARPS * a.ra.norm_dim * 4) smem = (size_t)NR_WARPS * a.ra.norm_dim * 4;
     const void* fn = bwd ? (const void*)norm_rope_bwd_kernel<T, G, NC> : (const void*)norm_rope_kernel<T, G, NC>;
     if (smem > 48 * 1024 &&
@@ -359,8 +398,7 @@ bool launch_norm_rope_bwd(const NormRopeArgs& in, bool bf16, float* dw, cudaStre
         ok = bf16 ? nr_launch_dim<__nv_bfloat16>(a, true, blocks, s) : nr_launch_dim<float>(a, true, blocks, s);
     }
     if (!ok || !a.dw_part) return ok;
-    norm_rope_dw_kernel<<<(n + 31) / 32, dim3(32, 32), 0, s>>>(a.dw_part, blocks, n, dw);
-    return cudaGetLastError() == cudaSuccess;
+    return launch_after(norm_rope_dw_kernel, dim3((n + 31) / 32), dim3(32, 32), s, (const float*)a.dw_part, blocks, n, dw);
 }
 
 }  // namespace dsa

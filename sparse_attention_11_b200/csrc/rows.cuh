@@ -8,21 +8,43 @@
 namespace dsa {
 
 // ---------------------------------------------------------------------------
+// A kernel that starts while the one before it on the stream ends: it calls
+// grid_wait() before it reads what that one wrote.
+// ---------------------------------------------------------------------------
+DSA_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P, class... A>
+bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess;
+}
+
+// ---------------------------------------------------------------------------
 // Page table: the pool row of a sequence's position.
 // ---------------------------------------------------------------------------
 struct PageRef {
     int64_t page;  // -1: no valid page
     int32_t slot;  // row inside the page
 };
+DSA_DEV void page_split(const PageView& pv, uint32_t s, uint32_t& p, uint32_t& o) {  // s = p * page_size + o
+    if (pv.shift >= 0) {
+        p = s >> pv.shift;
+        o = s & (uint32_t)(pv.page_size - 1);
+    } else {
+        p = s / (uint32_t)pv.page_size;
+        o = s - p * (uint32_t)pv.page_size;
+    }
+}
 DSA_DEV PageRef page_of(const PageView& pv, int b, int64_t s) {
     uint32_t p, o;
-    if (pv.shift >= 0) {
-        p = (uint32_t)s >> pv.shift;
-        o = (uint32_t)s & (uint32_t)(pv.page_size - 1);
-    } else {
-        p = (uint32_t)s / (uint32_t)pv.page_size;
-        o = (uint32_t)s - p * (uint32_t)pv.page_size;
-    }
+    page_split(pv, (uint32_t)s, p, o);
     PageRef r;
     r.slot = (int32_t)o;
     r.page = (int64_t)p < pv.ld_table ? (int64_t)__ldg(pv.table + b * pv.ld_table + p) : -1;
@@ -31,21 +53,12 @@ DSA_DEV PageRef page_of(const PageView& pv, int b, int64_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// 8 consecutive elements as floats (two 16-byte accesses for fp32, one for bf16)
+// 8 consecutive elements (two 16-byte accesses for fp32, one for bf16)
 // ---------------------------------------------------------------------------
 DSA_DEV void load8(const float* p, float (&v)[8]) {
     const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-DSA_DEV void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = *(const uint4*)p;
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
 }
 DSA_DEV void store8(float* p, const float (&v)[8]) {
     *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
@@ -69,9 +82,38 @@ DSA_DEV float group_sum(float x) {
 // Rotate the chunks of this row that lie in the rotated columns, in place;
 // sgn = 1 rotates by the position's angles, -1 back (the transpose).
 // Interleaved pairs lie inside an 8-column chunk.  Half-split pairs are
-// rope_dim / 2 columns apart, in another lane's chunk: the rotated columns pass
-// through `sm`, this row group's rope_dim floats of shared memory.  All lanes
-// of the warp call this together.
+// rope_dim / 2 columns apart: in another chunk of the same lane where that is
+// a multiple of 8 G columns (heads of 128 and 256 columns, rotated whole), else in
+// another lane's chunk, and the rotated columns pass through `sm`, this row
+// group's rope_dim floats of shared memory.  All lanes of the warp call this
+// together.
+template <int G, int NC, int D>
+DSA_DEV void rotate_in_lane(float (&v)[NC][8], const RowXform& ra, const float* __restrict__ cs, int gl, float sgn, bool live) {
+    const int h = ra.rope_dim >> 1;
+#pragma unroll
+    for (int i = 0; i + D < NC; ++i) {
+        const int o = (gl + G * i) * 8 - ra.rope_begin;  // the partner is at o + h
+        if (live && o >= 0 && o < h) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 c4 = __ldg((const float4*)(cs + o) + x), s4 = __ldg((const float4*)(cs + h + o) + x);
+                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x * sgn, s4.y * sgn, s4.z * sgn, s4.w * sgn};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = v[i][4 * x + e], b = v[i + D][4 * x + e];
+                    v[i][4 * x + e] = a * c[e] - b * s[e];
+                    v[i + D][4 * x + e] = b * c[e] + a * s[e];
+                }
+            }
+        }
+    }
+}
+// chunks between the halves of a pair, 0: in another lane
+template <int G>
+__host__ __device__ inline int rope_in_lane(const RowXform& ra) {
+    const int h = ra.rope_dim >> 1;
+    return !ra.interleaved && (h == 8 * G || h == 16 * G) ? h / (8 * G) : 0;
+}
 template <int G, int NC>
 DSA_DEV void rotate_chunks(float (&v)[NC][8], const RowXform& ra, const float* __restrict__ cs, int gl, float sgn, bool live,
                            float* sm) {
@@ -94,6 +136,11 @@ DSA_DEV void rotate_chunks(float (&v)[NC][8], const RowXform& ra, const float* _
             }
         }
         return;
+    }
+    if constexpr (NC > 1) {
+        const int d = rope_in_lane<G>(ra);
+        if (d == 1) return rotate_in_lane<G, NC, 1>(v, ra, cs, gl, sgn, live);
+        if (NC > 2 && d == 2) return rotate_in_lane<G, NC, 2>(v, ra, cs, gl, sgn, live);
     }
     __syncwarp();  // the previous row's reads of sm are done
 #pragma unroll
@@ -123,25 +170,55 @@ DSA_DEV void rotate_chunks(float (&v)[NC][8], const RowXform& ra, const float* _
     }
 }
 
-// One row by a group of G lanes (lane gl of the group holds the 8-column
-// chunks gl, gl + G, ...): norm, weight, rotation, one rounding to T.
-// x and y may be the same row.  cs: the position's cos | sin row.
+// A row as loaded: this lane's chunks gl, gl + G, ... of 8 columns each,
+// unconverted, so that the next row can be in flight while one is worked on.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+};
+DSA_DEV void unpack8(const Raw8<float>& r, float (&v)[8]) {
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
+    v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
+}
+DSA_DEV void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+// columns [0, cols) of row x (zeros past them, or everywhere if !have)
 template <class T, int G, int NC>
-DSA_DEV void row_forward(const T* x, T* y, const RowXform& ra, int dim, const float* __restrict__ cs, int gl,
-                         bool live, float* sm) {
-    float v[NC][8];
-    float ss = 0.f;
+DSA_DEV void load_row(Raw8<T> (&r)[NC], const T* x, int cols, int gl, bool have) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = (gl + G * i) * 8;
-        if (live && c < dim) {
-            load8(x + c, v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        }
+        r[i] = Raw8<T>{};
+        if (have && c < cols) r[i] = *(const Raw8<T>*)(x + c);
     }
+}
+DSA_DEV void load_weight8(const float* __restrict__ weight, int c, float (&w)[8]) {
+    const float4 a = __ldg((const float4*)(weight + c)), b = __ldg((const float4*)(weight + c) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// One loaded row by a group of G lanes: norm, weight, rotation, one rounding to
+// T, stored to y if live.  cs: the position's cos | sin row.
+template <class T, int G, int NC>
+DSA_DEV void row_forward(const Raw8<T> (&r)[NC], T* y, const RowXform& ra, int dim, const float* __restrict__ cs, int gl,
+                         bool live, float* sm) {
+    float v[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) unpack8(r[i], v[i]);
     if (ra.norm_dim > 0) {
+        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
             if ((gl + G * i) * 8 < ra.norm_dim)
@@ -154,10 +231,7 @@ DSA_DEV void row_forward(const T* x, T* y, const RowXform& ra, int dim, const fl
             const int c = (gl + G * i) * 8;
             if (c < ra.norm_dim) {
                 float w[8];
-                if (ra.weight) {
-                    const float4 a = __ldg((const float4*)(ra.weight + c)), b = __ldg((const float4*)(ra.weight + c) + 1);
-                    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-                }
+                if (ra.weight) load_weight8(ra.weight, c, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[i][e] = ra.weight ? v[i][e] * rstd * w[e] : v[i][e] * rstd;
             }
