@@ -448,7 +448,9 @@ typedef struct dsa_append_args {
  * idx_new in 64 bits; FP8: scale = fp32(amax / 448) (1 when that is 0), codes =
  * the e4m3 values nearest to key / scale (ties to even, saturating).  All other
  * rows of the pools keep their contents.  Two tokens of one call must not map to
- * the same row.  Workspace: a status header. */
+ * the same row.  A token without a valid position or page, or past the cos_sin
+ * rows of a part that rotates, is recorded as DSA_ERR_INDEX and not appended.
+ * Workspace: a status header. */
 DSA_API int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_append_args* ap, void* ws,
                              size_t ws_bytes, dsa_stream_t stream);
 

@@ -19,11 +19,8 @@
 namespace dsa {
 
 constexpr int PS_KEYS = 128;  // keys per tile
-constexpr int PS_NST = 4;     // key stages
-constexpr int PS_EPI = 4;     // epilogue warps 0..3 (TMEM lane quadrants)
-constexpr int PS_PROD = 4;    // producer warps 4..7
-constexpr int PS_MMA_WARP = 8;
-constexpr int PS_THREADS = 32 * 9;
+constexpr int PS_NST = 4;     // key stages (three measured the same; six leave two CTAs an SM: 111 against 87 us)
+constexpr int PS_PROD = 4;    // producer warps
 constexpr uint32_t PS_STAGE = PS_KEYS * 128;
 
 template <int NQ>
@@ -33,6 +30,11 @@ struct PsSmem {
     static constexpr uint32_t OFF_BAR = OFF_SROW + NQ * 4;
     static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // + alignment
     static constexpr uint32_t TMEM_COLS = 2 * NQ < 32 ? 32 : 2 * NQ;
+    // Warps: the epilogue's (one per TMEM lane quadrant and 64 queries), producers, MMA
+    static constexpr int EPI = NQ > 64 ? 8 : 4;
+    static constexpr int HALF = NQ / (EPI / 4);  // queries of an epilogue warp
+    static constexpr int MMA_WARP = EPI + PS_PROD;
+    static constexpr int THREADS = 32 * (MMA_WARP + 1);
 };
 struct PsBars {
     uint64_t full[PS_NST], empty[PS_NST];
@@ -50,12 +52,13 @@ DSA_DEV float ps_relu(float x) {  // as the packed scores: -0 and below to +0, N
 }
 
 template <int NQ>
-__global__ void __launch_bounds__(PS_THREADS) paged_scores_kernel(const PagedScoresArgs a) {
+__global__ void __launch_bounds__(PsSmem<NQ>::THREADS) paged_scores_kernel(const PagedScoresArgs a) {
     using Lay = PsSmem<NQ>;
     extern __shared__ uint8_t ps_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)ps_raw + 1023) & ~(uintptr_t)1023);
     PsBars* bars = (PsBars*)(smem + Lay::OFF_BAR);
     float* srow = (float*)(smem + Lay::OFF_SROW);
+    constexpr int PS_EPI = Lay::EPI, PS_MMA_WARP = Lay::MMA_WARP, PS_THREADS = Lay::THREADS;
     const int warp = (int)warp_id(), lane = (int)lane_id();
     volatile int* abort = &bars->abort;
     StatusHdr* st = a.st;
@@ -171,46 +174,87 @@ __global__ void __launch_bounds__(PS_THREADS) paged_scores_kernel(const PagedSco
             mbar_wait(smem_u32(&bars->drain), 0, nullptr, st, 0x4203, 1ll << 28);
         }
     } else {
-        // ================= epilogue: one thread per key =================
+        // ================= epilogue: one thread per key (and 64 queries) =================
+        const int quad = warp & 3, ch = warp >> 2;
         float* out = a.scores + (t_first - a.row_begin) * a.ld;
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const float none = a.fill ? -INFINITY : 0.f;  // the selection's own scores are never negative
-        auto scale_of = [&](int64_t tile, bool& ok) -> float {
-            const int64_t s = tile * PS_KEYS + warp * 32 + lane;
-            ok = true;
+        // rows of this warp, from a whole group of 16
+        const int c_beg = max(r_lo & ~15, ch * Lay::HALF), c_end = min(r_hi, (ch + 1) * Lay::HALF);
+        // A key's scale takes two dependent loads: pages are read three tiles ahead,
+        // scales two, so that neither is waited for.
+        const int32_t* table = a.pv.table + b * a.pv.ld_table;
+        auto page_at = [&](int64_t tile, int& slot) -> int32_t {
+            const int64_t s = tile * PS_KEYS + quad * 32 + lane;
+            slot = 0;
+            if (tile >= t_act || s > pos_last) return 0;  // no row sees it
+            uint32_t p, o;
+            page_split(a.pv, (uint32_t)s, p, o);
+            slot = (int)o;
+            return (int64_t)p < a.pv.ld_table ? __ldg(table + p) : -1;
+        };
+        auto scale_at = [&](int64_t tile, int32_t pg, int slot, bool& have) -> float {
+            const int64_t s = tile * PS_KEYS + quad * 32 + lane;
+            have = true;
             if (tile >= t_act || s > pos_last) return 0.f;
-            const PageRef pr = page_of(a.pv, b, s);
-            ok = pr.page >= 0;
-            if (!ok) {
+            have = (uint32_t)pg < (uint32_t)a.pv.num_pages;
+            if (!have) {
                 report(st, DSA_ERR_INDEX, t_first);
                 return 0.f;
             }
-            return __ldg(a.k_scale + pr.page * a.scale_page_stride + pr.slot);
+            return __ldg(a.k_scale + (int64_t)pg * a.scale_page_stride + slot);
         };
-        bool nok;
-        float nks = scale_of(t_lo, nok);
+        int sl0, sl1, sl2;
+        const int32_t pg0 = page_at(t_lo, sl0), pg1 = page_at(t_lo + 1, sl1);
+        int32_t pg2 = page_at(t_lo + 2, sl2);
+        bool h0, h1;
+        float k0 = scale_at(t_lo, pg0, sl0, h0), k1 = scale_at(t_lo + 1, pg1, sl1, h1);
         uint32_t g = 0;
         bool ok = true;
         for (int64_t tile = t_lo; ok && tile < t_act; ++tile, ++g) {
             const uint32_t ab = g & 1;
-            const float ks = nks;
-            const bool have = nok;
-            nks = scale_of(tile + 1, nok);
+            const float ks = k0;
+            const bool have = h0;
+            k0 = k1, h0 = h1;
+            k1 = scale_at(tile + 2, pg2, sl2, h1);
+            pg2 = page_at(tile + 3, sl2);
             if (!wait_warp(smem_u32(&bars->acc_full[ab]), (g >> 1) & 1, abort, st, 0x4301)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int64_t s = tile * PS_KEYS + warp * 32 + lane;
+            const int64_t s = tile * PS_KEYS + quad * 32 + lane;
             const bool in = s < a.cols;
-            for (int c0 = 0; c0 < r_hi; c0 += 16) {
+            const int64_t end = (tile + 1) * PS_KEYS;  // every row asked for sees the whole tile
+            const bool whole = end <= a.cols && end - 1 <= pos_first + r_lo;
+            if (c_beg >= c_end) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[ab]));
+            }
+            for (int c0 = c_beg; c0 < c_end; c0 += 16) {
                 uint32_t acc[16];
                 tmem_ld16(tmem + lane_off + ab * NQ + c0, acc);
                 tmem_wait_ld();
-                if (c0 + 16 >= r_hi) {  // the last columns read: hand the accumulator back
+                if (c0 + 16 >= c_end) {  // the last columns read: hand the accumulator back
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[ab]));
+                }
+                if (whole && c0 >= r_lo && c0 + 16 <= r_hi) {
+                    float* o = out + (int64_t)c0 * a.ld + s;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 f = *(const float4*)(srow + c0 + 4 * q);
+                        const float fr[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = ps_relu(__fmul_rn(__fmul_rn(__uint_as_float(acc[4 * q + e]), ks), fr[e]));
+                            *o = have ? x : none;
+                            o += a.ld;
+                        }
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -225,9 +269,9 @@ __global__ void __launch_bounds__(PS_THREADS) paged_scores_kernel(const PagedSco
         }
         if (a.fill)  // tiles past every row's position
             for (int64_t tile = t_act; tile < t_hi; ++tile) {
-                const int64_t s = tile * PS_KEYS + warp * 32 + lane;
+                const int64_t s = tile * PS_KEYS + quad * 32 + lane;
                 if (s < a.cols)
-                    for (int r = r_lo; r < r_hi; ++r) out[(int64_t)r * a.ld + s] = -INFINITY;
+                    for (int r = max(r_lo, ch * Lay::HALF); r < c_end; ++r) out[(int64_t)r * a.ld + s] = -INFINITY;
             }
     }
     tc_fence_before();
@@ -295,17 +339,21 @@ static bool ps_launch(PagedScoresArgs a, cudaStream_t s) {
     const int64_t tiles = (a.cols + PS_KEYS - 1) / PS_KEYS;
     const int64_t units = (a.max_seqlen_q + NQ - 1) / NQ * a.sv.batch;
     if (tiles <= 0 || units <= 0) return true;
-    // key tiles a CTA: about four CTAs for every two that are resident on an SM, and
-    // at least four tiles, so that the start of a CTA is hidden by its neighbour
-    int64_t per = (tiles * units + 148 * 8 - 1) / (148 * 8);
-    per = per < 4 ? 4 : per > 64 ? 64 : per;
+    // Key tiles a CTA.  Few queries: eight CTAs an SM (three are resident), so that
+    // sequences of different lengths even out (16K to 64K keys: 87 us; four 89,
+    // sixteen 90, thirty-two 106).  Blocks of 128 queries: as many CTAs as are
+    // resident for one sequence (1000 x 32000: 33 us against 36 with four an SM),
+    // twice that for several.
+    const int64_t ctas = 148 * (NQ <= 16 ? 8 : a.sv.batch == 1 ? 2 : 4), least = NQ <= 16 ? 4 : 2;
+    int64_t per = (tiles * units + ctas - 1) / ctas;
+    per = per < least ? least : per > 64 ? 64 : per;
     a.tiles_per_cta = (int)per;
     const int64_t grid = (tiles + per - 1) / per * units;
     if (grid >= ((int64_t)1 << 31)) return false;
     if (cudaFuncSetAttribute(paged_scores_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)PsSmem<NQ>::SMEM) != cudaSuccess)
         return false;
-    paged_scores_kernel<NQ><<<(unsigned)grid, PS_THREADS, PsSmem<NQ>::SMEM, s>>>(a);
+    paged_scores_kernel<NQ><<<(unsigned)grid, PsSmem<NQ>::THREADS, PsSmem<NQ>::SMEM, s>>>(a);
     return cudaGetLastError() == cudaSuccess;
 }
 

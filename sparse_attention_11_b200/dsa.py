@@ -119,11 +119,14 @@ def _check(code, where):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream's handle (without torch.cuda.current_stream's object,
+    which costs 3 us a call)."""
+    torch.cuda._lazy_init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def status_string(code):
@@ -289,7 +292,7 @@ def _dtype(t):
 def _here(t):
     """Refuse tensors of another device than the current one, whose stream the
     call would use."""
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), "tensors must be on the current CUDA device")
+    _need(t.is_cuda and t.get_device() == torch._C._cuda_getDevice(), "tensors must be on the current CUDA device")
 
 
 def rope_table(positions, dim, base=10000.0, device="cuda"):
@@ -389,33 +392,38 @@ def paged_attn_args(pages, q, scale, out, lse=None):
     return a
 
 
-def _rows_of(seqs, t, dtype):
-    _need(t.dim() == 3 and t.shape[0] >= seqs.total_q and t.stride(2) == 1 and t.dtype == dtype,
-          "rows: [T, heads, dim] of one type, contiguous")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _rows_of(seqs, t, shape, dtype):
+    s = t.stride()
+    if t.shape != shape or len(s) != 3 or shape[0] < seqs.c.total_q or (s[2] != 1 and shape[2] > 1) or t.dtype != dtype:
+        raise ValueError("rows: [T, heads, dim] of one shape and type, contiguous columns")
+    return t.data_ptr(), s[0], s[1]
 
 
 def dsa_norm_rope(seqs, ra, x, y, ws):
     """y[t,h,:] = the transform ra (row_args or None) of x[t,h,:] at token t's
     position; x, y [T,H,dim] bfloat16 or float32 (y may be x)."""
     _here(x)
-    _check(_lib.dsa_norm_rope(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(x), x.shape[1],
-                              x.shape[2], *_rows_of(seqs, x, x.dtype), *_rows_of(seqs, y, x.dtype), _ptr(ws), ws.numel(),
-                              _stream()), "dsa_norm_rope")
+    sh, dt = x.shape, x.dtype
+    xp, xt, xh = _rows_of(seqs, x, sh, dt)
+    yp, yt, yh = _rows_of(seqs, y, sh, dt)
+    _check(_lib.dsa_norm_rope(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(x), sh[1], sh[2],
+                              xp, xt, xh, yp, yt, yh, ws.data_ptr(), ws.numel(), _stream()), "dsa_norm_rope")
 
 
 def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
     """Backward of dsa_norm_rope: d_x [T,H,dim] (x's type) and d_weight (float32
-    [norm_dim] or None) are written from x and d_y.  ws of
+    [norm_dim] or None) are written from x (None without a norm) and d_y.  ws of
     dsa_workspace_size(DSA_OP_NORM_ROPE_BWD, seqs, norm_dim) bytes."""
     _here(d_y)
-    _need(x.shape == d_y.shape == d_x.shape, "x, d_y and d_x have one shape")
+    sh, dt = d_y.shape, d_y.dtype
+    xp, xt, xh = _rows_of(seqs, x, sh, dt) if x is not None else (None, sh[1] * sh[2], sh[2])
+    gp, gt, gh = _rows_of(seqs, d_y, sh, dt)
+    dp, dt_, dh = _rows_of(seqs, d_x, sh, dt)
     _need(d_weight is None or (d_weight.dtype == torch.float32 and d_weight.is_contiguous()
                                and d_weight.numel() == (ra.norm_dim if ra is not None else 0)),
           "d_weight: contiguous float32 [norm_dim]")
     _check(_lib.dsa_norm_rope_bwd(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(d_y),
-                                  d_y.shape[1], d_y.shape[2], *_rows_of(seqs, x, d_y.dtype),
-                                  *_rows_of(seqs, d_y, d_y.dtype), *_rows_of(seqs, d_x, d_y.dtype), _ptr(d_weight), _ptr(ws),
+                                  sh[1], sh[2], xp, xt, xh, gp, gt, gh, dp, dt_, dh, _ptr(d_weight), ws.data_ptr(),
                                   ws.numel(), _stream()), "dsa_norm_rope_bwd")
 
 
