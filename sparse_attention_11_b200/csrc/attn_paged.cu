@@ -127,7 +127,7 @@ DSA_DEV PaItem pa_item(const PagedAttnArgs& a, int64_t grp, int part, int sel_pa
     PaItem it = {};
     int b;
     if (!DENSE || a.group == 1) {
-        const RowInfo ri = row_info(a.sv, grp);
+        const RowInfo ri = row_info_guess(a.sv, grp, a.total_q);
         it.t0 = grp;
         it.b = ri.b;
         it.pos0 = ri.pos;
@@ -244,6 +244,62 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         if (lane == 0) mbar_arrive(smem_u32(&bars->info_empty[qi & 1]));
     };
 
+    // Q of an item: three blocks into shared memory, six through registers and
+    // this warp's staging tile (a row a lane) into tensor memory.  Rows past the
+    // item are zero.  Loads take 4 rows x 128 bytes an instruction: a row a lane
+    // costs 32 cache lines each (9200 cycles an item, now about 2500).
+    // wait: until the last S of the item before has completed
+    auto load_q = [&](const PaItem& it, int quad, uint8_t* stg, auto wait) -> bool {
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const int sub = lane >> 3, chunk = lane & 7;
+        int64_t off[8];  // rows 4 j + sub of this warp
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = quad * 32 + 4 * j + sub, tk = r / a.heads;
+            off[j] = tk < it.ntok ? (it.t0 + tk) * a.q_stride_tok + (int64_t)(r - tk * a.heads) * a.q_stride_head + chunk * 8
+                                  : -1;
+        }
+        const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
+        uint4 x[8];
+        auto fetch = [&](int blk) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = off[j] >= 0 ? __ldg((const uint4*)(q + off[j] + blk * 64)) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto blk_of = [&](int i) { return i < 2 ? kblk(3 + i) : vblk(i - 2); };  // tensor-memory blocks in their order
+        fetch(blk_of(0));
+        if (!wait()) return false;
+        tc_fence_after();
+        const uint32_t sq = smem_u32(smem + Lay::OFF_Q);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                cp_async16_n(sq + i * PA_QBLK + pa_swz(quad * 32 + 4 * j + sub, chunk),
+                             q + (off[j] >= 0 ? off[j] + kblk(i) * 64 : 0), off[j] >= 0 ? 16u : 0u);
+#pragma unroll 1
+        for (int i = 0; i < 6; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *(uint4*)(stg + pa_swz(4 * j + sub, chunk)) = x[j];
+            __syncwarp();
+            if (i < 5) fetch(blk_of(i + 1));
+            uint32_t r[32];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint4 v = *(const uint4*)(stg + pa_swz(lane, c));
+                r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+            }
+            tmem_st32(tmem + lane_off + PA_TM_Q + i * 32, r);
+            __syncwarp();
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tmem_wait_st();
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        return true;
+    };
+
     if (warp >= PA_PROD0 && warp < PA_MMA) {
         // ================= gather producers =================
         const int pw = warp - PA_PROD0;
@@ -253,6 +309,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         uint32_t g = 0;  // tile of the CTA's whole sequence
         bool ok = true;
         const __nv_bfloat16* pool = (const __nv_bfloat16*)a.k + chunk * 8;
+        // the first item's first two tiles into L2, before its info is there
+        if (nq > 0) {
+            const int64_t grp = item0 / a.splits;
+            const PaItem it = pa_item<DENSE>(a, grp, (int)(item0 - grp * a.splits), sel_part);
+            for (int key = 4 * pw + sub; key < min(2 * PA_N, it.count); key += 4 * PA_PRODUCERS) {
+                const int32_t v = DENSE ? it.lo + key : __ldg(a.idx + it.t0 * a.ld_idx + it.lo + key);
+                if (v < 0 || v >= it.seqlen_k) continue;
+                const PageRef pr = page_of(a.pv, it.b, v);
+                if (pr.page < 0) continue;
+                const __nv_bfloat16* row = (const __nv_bfloat16*)a.k + pr.page * a.k_page_stride + (int64_t)pr.slot * a.k_stride;
+                prefetch_l2(row + chunk * 64);
+                if (chunk == 0) prefetch_l2(row + 512);
+            }
+        }
         for (int64_t qi = 0; ok && qi < nq; ++qi) {
             if (!info_wait(qi, 0x2103)) break;
             const PaItem it = items[qi & 1];
@@ -457,6 +527,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         float* xm = (float*)(smem + Lay::OFF_XM);
         uint32_t g = 0, e = 0;
         bool ok = true;
+        // the first item's Q, while the epilogue warps read its selection (staged in
+        // P's buffer; not used if the item turns out empty)
+        if (kh == 0 && nq > 0) {
+            const int64_t grp = item0 / a.splits;
+            load_q(pa_item<DENSE>(a, grp, (int)(item0 - grp * a.splits), sel_part), quad, smem + Lay::OFF_P + quad * 4096,
+                   [] { return true; });
+            if (!info_wait(0, 0x2301)) ok = false;
+            else if (tiles_of(0) > 0 && lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+            __syncwarp();
+        }
         for (int64_t qi = 0; ok && qi < nq; ++qi) {
             if (!info_wait(qi, 0x2301)) break;
             const int n_tiles = tiles_of(qi);
@@ -694,61 +774,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             __syncwarp();
             return true;
         };
-        // Q of an item: three blocks into shared memory, six through registers and
-        // this warp's staging tile (a row a lane) into tensor memory.  Rows past the
-        // item are zero.  Loads take 4 rows x 128 bytes an instruction: a row a lane
-        // costs 32 cache lines each (9200 cycles an item, now about 2500).
-        auto load_q = [&](const PaItem& it, uint32_t e) -> bool {
-            const int sub = lane >> 3, chunk = lane & 7;
-            int64_t off[8];  // rows 4 j + sub of this warp
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = quad * 32 + 4 * j + sub, tk = r / a.heads;
-                off[j] = tk < it.ntok ? (it.t0 + tk) * a.q_stride_tok + (int64_t)(r - tk * a.heads) * a.q_stride_head + chunk * 8
-                                      : -1;
-            }
-            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q;
-            uint4 x[8];
-            auto fetch = [&](int blk) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = off[j] >= 0 ? __ldg((const uint4*)(q + off[j] + blk * 64)) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            auto blk_of = [&](int i) { return i < 2 ? kblk(3 + i) : vblk(i - 2); };  // tensor-memory blocks in their order
-            fetch(blk_of(0));
-            if (e > 0 && !wait_warp(smem_u32(&bars->q_free), (e - 1) & 1, abort, st, 0x2404)) return false;
-            tc_fence_after();
-            const uint32_t sq = smem_u32(smem + Lay::OFF_Q);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    cp_async16_n(sq + i * PA_QBLK + pa_swz(quad * 32 + 4 * j + sub, chunk),
-                                 q + (off[j] >= 0 ? off[j] + kblk(i) * 64 : 0), off[j] >= 0 ? 16u : 0u);
-#pragma unroll 1
-            for (int i = 0; i < 6; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) *(uint4*)(stg + pa_swz(4 * j + sub, chunk)) = x[j];
-                __syncwarp();
-                if (i < 5) fetch(blk_of(i + 1));
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 v = *(const uint4*)(stg + pa_swz(lane, c));
-                    r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
-                }
-                tmem_st32(tmem + lane_off + PA_TM_Q + i * 32, r);
-                __syncwarp();
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            tmem_wait_st();
-            fence_proxy_async();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
-            return true;
-        };
-
         uint32_t e = 0;     // items with tiles begun
         bool ok = nq == 0 || publish(0), pend = false;  // the (e - 1)-th item's epilogue is still to be done
         int64_t item_pend = 0;
@@ -758,7 +783,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             if (!info_wait(qi, 0x2403)) { ok = false; break; }
             const PaItem it = items[qi & 1];
             const int n_tiles = tiles_of(qi);
-            if (n_tiles > 0 && !load_q(it, e)) { ok = false; break; }
+            if (n_tiles > 0 && qi > 0) {  // (the first item's Q: the softmax warps)
+                // (an empty first item: its Q, unused, must have landed; later items' info
+                // was published after that)
+                auto wait = [&]() {
+                    if (e > 0) return wait_warp(smem_u32(&bars->q_free), (e - 1) & 1, abort, st, 0x2404);
+                    return qi > 1 || wait_warp(smem_u32(&bars->info_empty[0]), 0, abort, st, 0x2405);
+                };
+                if (!load_q(it, quad, stg, wait)) { ok = false; break; }
+                if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+            }
             // ---- the previous item's epilogue (this item's first S overlaps it) ----
             if (pend && !epilogue(it_pend, item_pend, e - 1)) { ok = false; break; }
             pend = false;

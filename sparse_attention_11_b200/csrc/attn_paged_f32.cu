@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32) attn_paged_f32_kernel(const Pag
     const int warp = (int)warp_id(), lane = (int)lane_id();
     const int64_t t = blockIdx.x / (unsigned)a.splits;
     const int part = (int)(blockIdx.x - t * a.splits);
-    const RowInfo ri = row_info(a.sv, t);
+    const RowInfo ri = row_info_guess(a.sv, t, a.total_q);
     if (!ri.ok) {  // rows without a valid position are left as they were
         if (threadIdx.x == 0) report(a.st, DSA_ERR_INDEX, t);
         return;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32) attn_paged_f32_kernel(const Pag
 __global__ void __launch_bounds__(128) attn_paged_f32_combine_kernel(const PagedAttnArgs a) {
     const int64_t t = blockIdx.x;
     const int lane = (int)lane_id();
-    if (!row_info(a.sv, t).ok) return;  // left as it was
+    if (!row_info_guess(a.sv, t, a.total_q).ok) return;  // left as it was
     grid_wait();
     for (int h = (int)warp_id(); h < a.heads; h += 4) {
         // lane p holds the weights of parts p and p + 32

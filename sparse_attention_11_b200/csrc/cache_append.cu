@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(AP_WARPS * 32) cache_append_kernel(const Appen
         for (int e = 0; e < 4; ++e) kx[e] = load1((const T*)a.idx_new + t * a.idx_new_stride + 4 * lane + e);
     }
     if constexpr (NC > 0) load_row<T, 32, NC>(row, x, a.dim, lane, a.kv_new != nullptr);
-    const RowInfo ri = row_info(a.sv, t);
+    const RowInfo ri = row_info_guess(a.sv, t, a.total_q);
     PageRef pr;
     pr.page = -1;
     pr.slot = 0;

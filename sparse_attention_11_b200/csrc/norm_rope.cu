@@ -32,12 +32,13 @@ struct TokenPos {
     bool ok = false;
     const float* cs = nullptr;
 };
-DSA_DEV void token_pos(TokenPos& tp, int64_t t, const SeqView& sv, const RowXform& ra, StatusHdr* st) {
+DSA_DEV void token_pos(TokenPos& tp, int64_t t, const NormRopeArgs& a) {
+    const RowXform& ra = a.ra;
     if (t == tp.t) return;
     tp.t = t;
-    const RowInfo ri = row_info(sv, t);
+    const RowInfo ri = row_info_guess(a.sv, t, a.total_q);
     tp.ok = ri.ok && (ra.rope_dim == 0 || ri.pos < ra.rope_positions);
-    if (!tp.ok) report(st, DSA_ERR_INDEX, t);
+    if (!tp.ok) report(a.st, DSA_ERR_INDEX, t);
     tp.cs = tp.ok && ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr;
 }
 
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 4 : 1) norm_rope_kernel(
         Raw8<T> cur[NC];
         load_row<T, G, NC>(cur, (const T*)a.x + w.t * a.x_stride_tok + w.h * a.x_stride_head, a.dim, gl, live);
         if (live) {
-            token_pos(tp, w.t, a.sv, a.ra, a.st);
+            token_pos(tp, w.t, a);
             live = tp.ok;
         }
         row_forward<T, G, NC>(cur, (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head, a.ra, a.dim, tp.cs, gl, live, sm);
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_scalar_kernel(const Norm
     TokenPos tp;
     for (int64_t r = (int64_t)blockIdx.x * NR_WARPS + warp_id(); r < rows; r += step) {
         const int64_t t = r / a.heads, h = r - t * a.heads;
-        token_pos(tp, t, a.sv, a.ra, a.st);
+        token_pos(tp, t, a);
         if (!tp.ok) continue;
         row_forward_scalar<T>((const T*)a.x + t * a.x_stride_tok + h * a.x_stride_head,
                               (T*)a.y + t * a.y_stride_tok + h * a.y_stride_head, a.ra, a.dim, tp.cs, (int)lane_id());
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
         else fetch(w, cx, cg);
         bool live = w.r < r_end;
         if (live) {
-            token_pos(tp, w.t, a.sv, a.ra, a.st);
+            token_pos(tp, w.t, a);
             live = tp.ok;
         }
         T* dx = (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const 
     TokenPos tp;
     for (int64_t r = (int64_t)blockIdx.x * NR_WARPS + warp; r < rows; r += step) {
         const int64_t t = r / a.heads, hd = r - t * a.heads;
-        token_pos(tp, t, a.sv, ra, a.st);
+        token_pos(tp, t, a);
         if (!tp.ok) continue;
         const T* x = (const T*)a.x + t * a.x_stride_tok + hd * a.x_stride_head;
         const T* dy = (const T*)a.dy + t * a.dy_stride_tok + hd * a.dy_stride_head;

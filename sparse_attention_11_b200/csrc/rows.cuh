@@ -26,6 +26,21 @@ bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A
     return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess;
 }
 
+// row_info of token t of total_q, after a first guess: sequences of equal length
+// (a decode batch) need no search, whose every step waits for a load.
+DSA_DEV RowInfo row_info_guess(const SeqView& sv, int64_t t, int64_t total_q) {
+    const int b = min(max((int)((float)t * ((float)sv.batch / (float)total_q)), 0), sv.batch - 1);
+    const int64_t q0 = __ldg(sv.cu_q + b), q1 = __ldg(sv.cu_q + b + 1), k0 = __ldg(sv.cu_k + b), k1 = __ldg(sv.cu_k + b + 1);
+    if (t < q0 || t >= q1) return row_info(sv, t);
+    RowInfo r;
+    r.b = b;
+    r.key_base = k0;
+    r.seqlen_k = k1 - k0;
+    r.pos = (k1 - k0) - (q1 - q0) + (t - q0);
+    r.ok = r.pos >= 0 && r.pos < r.seqlen_k;
+    return r;
+}
+
 // ---------------------------------------------------------------------------
 // Page table: the pool row of a sequence's position.
 // ---------------------------------------------------------------------------
