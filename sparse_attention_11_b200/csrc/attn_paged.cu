@@ -85,8 +85,8 @@ static_assert(2 * sizeof(PaItem) <= 128, "item ring");
 static_assert(PaLayout::SMEM <= 232448, "shared memory budget");
 
 struct PaBars {
-    uint64_t kfull[2], kfree[2];               // the two groups of the blocks that only S reads
-    uint64_t vfull[PA_NST], vfree[PA_NST];
+    uint64_t kfull, kfree[2];                // the two groups of the blocks that only S reads
+    uint64_t vfull[PA_NST], vfree[PA_NST];   // (vfull: of the second group too)
     uint64_t s_full, s_free;    // S complete / read by the softmax warps
     uint64_t p_full, p_free;    // P written (and O rescaled) / its PV complete
     uint64_t q_full, q_free;    // Q in place / its last S complete
@@ -197,10 +197,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
     auto kblk = [&](int i) { return i == 4 ? 8 : 4 * (half ^ 1) + i; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars->kfull[i]), PA_PRODUCERS * 32);
-            mbar_init(smem_u32(&bars->kfree[i]), 1);
-        }
+        mbar_init(smem_u32(&bars->kfull), PA_PRODUCERS * 32);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->kfree[i]), 1);
         for (int i = 0; i < PA_NST; ++i) {
             mbar_init(smem_u32(&bars->vfull[i]), PA_PRODUCERS * 32);
             mbar_init(smem_u32(&bars->vfree[i]), 1);
@@ -386,12 +384,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                 got = wait_warp(smem_u32(&bars->kfree[0]), (g & 1) ^ 1, abort, st, 0x2101);
                 if (got) {
                     copy(s_k, 0, 3, false);
-                    cp_async_arrive(smem_u32(&bars->kfull[0]));
+                    cp_async_arrive(smem_u32(&bars->kfull));
                     got = wait_warp(smem_u32(&bars->kfree[1]), (g & 1) ^ 1, abort, st, 0x2105);
                 }
                 if (got) {
                     copy(s_k, 3, 5, false);
-                    cp_async_arrive(smem_u32(&bars->kfull[1]));
                     got = wait_warp(smem_u32(&bars->vfree[s]), ((g / PA_NST) & 1) ^ 1, abort, st, 0x2104);
                 }
                 if (!got) { ok = false; break; }
@@ -402,112 +399,102 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == PA_MMA) {
         // ================= MMA issuer =================
-        // The warp runs only a few MMAs ahead of the tensor core, so a wait, even for a
-        // barrier that is long complete, idles it unless long MMAs are queued.  Hence
-        // three waits a tile, the two that may be long behind the MMAs of PV and of
-        // group 0.  Operands are constants or uniform: the tensor memory is all this
+        // One thread waits and issues, tile after tile: it runs only a few MMAs ahead of
+        // the tensor core, so every wait between its batches idles it, and a wait by the
+        // whole warp costs 115 cycles even for a barrier that is long complete, by one
+        // thread 56.  Operands are constants or uniform: the tensor memory is all this
         // CTA's, so it begins at column 0, and the V stage is a template argument.
         constexpr uint32_t idesc_s = idesc_make(1, 1, false, 128, PA_N);
         constexpr uint32_t idesc_pv = idesc_make(1, 1, true, 128, 256);
         const uint32_t base = smem_u32(smem);
         auto issue_sk = [&](auto grp_c) {  // S over group 0 (Q in shared memory) or 1 (in tensor memory)
             constexpr int grp = decltype(grp_c)::value;
-            if (elect_one()) {
 #pragma unroll
-                for (int i = grp ? 3 : 0; i < (grp ? 5 : 3); ++i)
+            for (int i = grp ? 3 : 0; i < (grp ? 5 : 3); ++i)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint64_t kd = sdesc_sw128(base + Lay::OFF_K + i * PA_BLK + ks * 32, 16, 1024);
-                        if (grp == 0)
-                            mma_bf16_ss(PA_TM_S, sdesc_sw128(base + Lay::OFF_Q + i * PA_QBLK + ks * 32, 16, 1024), kd, idesc_s,
-                                        (i | ks) ? 1u : 0u);
-                        else
-                            mma_bf16_ts(PA_TM_S, PA_TM_Q + (i - 3) * 32 + ks * 8, kd, idesc_s, 1u);
-                    }
-                mma_commit(smem_u32(&bars->kfree[grp]));
-            }
-            __syncwarp();
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t kd = sdesc_sw128(base + Lay::OFF_K + i * PA_BLK + ks * 32, 16, 1024);
+                    if (grp == 0)
+                        mma_bf16_ss(PA_TM_S, sdesc_sw128(base + Lay::OFF_Q + i * PA_QBLK + ks * 32, 16, 1024), kd, idesc_s,
+                                    (i | ks) ? 1u : 0u);
+                    else
+                        mma_bf16_ts(PA_TM_S, PA_TM_Q + (i - 3) * 32 + ks * 8, kd, idesc_s, 1u);
+                }
+            mma_commit(smem_u32(&bars->kfree[grp]));
         };
         auto issue_sv = [&](auto s_c, bool last) {
             constexpr uint32_t vst = Lay::OFF_V + decltype(s_c)::value * PA_VST;
-            if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ts(PA_TM_S, PA_TM_Q + (2 + i) * 32 + ks * 8,
-                                    sdesc_sw128(base + vst + i * PA_BLK + ks * 32, 16, 1024), idesc_s, 1u);
-                mma_commit(smem_u32(&bars->s_full));
-                if (last) mma_commit(smem_u32(&bars->q_free));
-            }
-            __syncwarp();
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ts(PA_TM_S, PA_TM_Q + (2 + i) * 32 + ks * 8,
+                                sdesc_sw128(base + vst + i * PA_BLK + ks * 32, 16, 1024), idesc_s, 1u);
+            mma_commit(smem_u32(&bars->s_full));
+            if (last) mma_commit(smem_u32(&bars->q_free));
         };
         auto issue_pv = [&](auto s_c, bool first, bool last) {
             constexpr uint32_t s = decltype(s_c)::value, vst = Lay::OFF_V + s * PA_VST;
-            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < PA_N / 16; ++ks)
-                    mma_bf16_ss(PA_TM_O, sdesc_noswz(base + Lay::OFF_P + ks * 4096, 2048, 128),
-                                sdesc_sw128(base + vst + ks * 2048, PA_BLK, 1024), idesc_pv, (!first || ks > 0) ? 1u : 0u);
-                mma_commit(smem_u32(&bars->vfree[s]));
-                mma_commit(smem_u32(&bars->p_free));
-                if (last) mma_commit(smem_u32(&bars->o_full));
-            }
-            __syncwarp();
+            for (int ks = 0; ks < PA_N / 16; ++ks)
+                mma_bf16_ss(PA_TM_O, sdesc_noswz(base + Lay::OFF_P + ks * 4096, 2048, 128),
+                            sdesc_sw128(base + vst + ks * 2048, PA_BLK, 1024), idesc_pv, (!first || ks > 0) ? 1u : 0u);
+            mma_commit(smem_u32(&bars->vfree[s]));
+            mma_commit(smem_u32(&bars->p_free));
+            if (last) mma_commit(smem_u32(&bars->o_full));
         };
         using C0 = std::integral_constant<int, 0>;
         using C1 = std::integral_constant<int, 1>;
         using C2 = std::integral_constant<int, 2>;
         static_assert(PA_NST == 3, "three V stages below");
-        // two barriers in one wait: even lanes poll the first, odd lanes the second
-        auto wait2 = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, int where) {
-            const bool got = wait_warp(smem_u32((lane & 1) ? b1 : b0), (lane & 1) ? p1 : p0, abort, st, where);
-            __syncwarp();
-            tc_fence_after();
-            return got;
-        };
         uint32_t g = 0, e = 0;  // tiles and items (with tiles) begun
-        bool ok = true, pend = false, pend_first = false, pend_last = false;  // PV(g - 1) is still to be issued
-        auto pv = [&]() -> bool {
-            const uint32_t p = g - 1, s = p % PA_NST;
-            // a first tile overwrites O: the epilogue of the item before (of those
-            // begun, the one before the pending tile's) has read it
-            const bool o_read = pend_first && e > 1;
-            if (!wait2(&bars->p_full, p & 1, o_read ? &bars->o_free : &bars->p_full, o_read ? (e & 1) : (p & 1), 0x2201))
-                return false;
-            if (s == 0) issue_pv(C0(), pend_first, pend_last);
-            else if (s == 1) issue_pv(C1(), pend_first, pend_last);
-            else issue_pv(C2(), pend_first, pend_last);
-            pend = false;
-            return true;
+        auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+            return mbar_wait(smem_u32(bar), parity, abort, st, where);
         };
-        for (int64_t qi = 0; ok && qi < nq; ++qi) {
-            if (!info_wait(qi, 0x2203)) { ok = false; break; }
-            const int n_tiles = tiles_of(qi);
-            info_done(qi);
-            if (n_tiles == 0) continue;
-            if (!wait_warp(smem_u32(&bars->q_full), e & 1, abort, st, 0x2204)) { ok = false; break; }
-            ++e;
-            for (int u = 0; u < n_tiles; ++u) {
+        // the tiles of an item
+        auto run = [&](int n_tiles) -> bool {
+            // PV of tile p; a first tile overwrites O, which the epilogue of the item
+            // before has read
+            auto pv = [&](uint32_t p, bool first, bool last) -> bool {
+                if (!wait(&bars->p_full, p & 1, 0x2201)) return false;
+                if (first && e > 0 && !wait(&bars->o_free, (e - 1) & 1, 0x2202)) return false;
+                tc_fence_after();
+                const uint32_t s = p % PA_NST;
+                if (s == 0) issue_pv(C0(), first, last);
+                else if (s == 1) issue_pv(C1(), first, last);
+                else issue_pv(C2(), first, last);
+                return true;
+            };
+            if (!wait(&bars->q_full, e & 1, 0x2204)) return false;
+            for (int u = 0; u < n_tiles; ++u, ++g) {
                 const uint32_t s = g % PA_NST;
-                if (!wait2(&bars->s_free, (g & 1) ^ 1, &bars->kfull[0], g & 1, 0x2205)) { ok = false; break; }
+                if (!wait(&bars->s_free, (g & 1) ^ 1, 0x2206) || !wait(&bars->kfull, g & 1, 0x2205)) return false;
                 fence_proxy_async();  // the rows arrived by cp.async (P's writers fence their own)
+                tc_fence_after();
                 issue_sk(C0());
-                if (!wait2(&bars->kfull[1], g & 1, &bars->vfull[s], (g / PA_NST) & 1, 0x2206)) { ok = false; break; }
+                if (!wait(&bars->vfull[s], (g / PA_NST) & 1, 0x2207)) return false;
                 fence_proxy_async();
                 issue_sk(C1());
                 const bool last = u + 1 == n_tiles;
                 if (s == 0) issue_sv(C0(), last);
                 else if (s == 1) issue_sv(C1(), last);
                 else issue_sv(C2(), last);
-                if (pend && !pv()) { ok = false; break; }
-                pend = true;
-                pend_first = u == 0;
-                pend_last = last;
-                ++g;
+                if (u > 0 && !pv(g - 1, u == 1, false)) return false;
             }
-            // the item's last PV, before anything of the next is waited for
-            if (ok && pend) ok = pv();
+            return pv(g - 1, n_tiles == 1, true);  // before anything of the next item is waited for
+        };
+        for (int64_t qi = 0; qi < nq; ++qi) {
+            if (!info_wait(qi, 0x2203)) break;
+            const int n_tiles = tiles_of(qi);
+            info_done(qi);
+            if (n_tiles == 0) continue;
+            bool ok = true;
+            const uint32_t g0 = g;
+            if (elect_one()) ok = run(n_tiles);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, ok)) break;
+            g = g0 + n_tiles;
+            ++e;
         }
         if (*abort) {
             if (elect_one()) {
