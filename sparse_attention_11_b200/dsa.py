@@ -113,6 +113,10 @@ class DsaError(RuntimeError):
         self.detail = detail
 
 
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
 def _check(code, where):
     if code != DSA_OK:
         raise DsaError(code, where)
@@ -125,8 +129,9 @@ def _ptr(t):
 def _stream():
     """The current stream's handle (without torch.cuda.current_stream's object,
     which costs 3 us a call)."""
-    torch.cuda._lazy_init()
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if not torch.cuda._initialized:
+        torch.cuda._lazy_init()
+    return _raw_stream(_device())
 
 
 def status_string(code):
@@ -292,7 +297,8 @@ def _dtype(t):
 def _here(t):
     """Refuse tensors of another device than the current one, whose stream the
     call would use."""
-    _need(t.is_cuda and t.get_device() == torch._C._cuda_getDevice(), "tensors must be on the current CUDA device")
+    if not t.is_cuda or t.get_device() != _device():
+        raise ValueError("tensors must be on the current CUDA device")
 
 
 def rope_table(positions, dim, base=10000.0, device="cuda"):
@@ -346,6 +352,7 @@ class Pages:
         _need(idx_scale is None or (idx_scale.dim() == 2 and idx_scale.dtype == torch.float32
                                     and (idx_scale.stride(1) == 1 or size == 1)), "idx_scale: float32 [pages, page_size]")
         self.table, self.kv, self.v, self.idx, self.idx_scale = table, kv, v, idx, idx_scale
+        self.batch = table.shape[0]
 
         def page(p):
             return 0 if p is None else p.stride(0)
@@ -373,6 +380,7 @@ def append_args(pages, kv_new=None, kv_row=None, idx_new=None, idx_row=None):
         a.idx_scale = pages.idx_scale.data_ptr() if pages.idx_scale is not None else None
         a.idx_row = ctypes.pointer(idx_row) if idx_row is not None else None
     a._keep = (pages, kv_new, kv_row, idx_new, idx_row)
+    a._rows = min(t.shape[0] for t in (kv_new, idx_new) if t is not None)
     return a
 
 
@@ -389,6 +397,7 @@ def paged_attn_args(pages, q, scale, out, lse=None):
                       kv.data_ptr(), kv.stride(1), v.data_ptr(), v.stride(1), float(scale), out.data_ptr(), out.stride(0),
                       out.stride(1), lse.data_ptr() if lse is not None else None)
     a._keep = (pages, q, out, lse)
+    a._rows = q.shape[0]
     return a
 
 
@@ -431,10 +440,10 @@ def dsa_cache_append(seqs, pages, ap, ws):
     """Append the queries' tokens (append_args) to the paged cache at their
     positions.  seqs holds the lengths after the append."""
     _here(pages.table)
-    _need(pages.table.shape[0] >= seqs.c.batch, "the table has a row per sequence")
-    for t in ap._keep[1], ap._keep[3]:
-        _need(t is None or t.shape[0] >= seqs.total_q, "a row per query token")
-    _check(_lib.dsa_cache_append(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ap), _ptr(ws), ws.numel(),
+    c = seqs.c
+    _need(pages.batch >= c.batch, "the table has a row per sequence")
+    _need(ap._rows >= c.total_q and ap._keep[0] is pages, "a row per query token, appended to these pages")
+    _check(_lib.dsa_cache_append(ctypes.byref(c), ctypes.byref(pages.c), ctypes.byref(ap), ws.data_ptr(), ws.numel(),
                                  _stream()), "dsa_cache_append")
 
 
@@ -443,16 +452,17 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
     indexer keys; scores float32 [row_count, >= max_seqlen_k], -inf past a row's
     position.  dsa_topk selects from them."""
     _here(u)
-    _need(pages.idx is not None and pages.table.shape[0] >= seqs.c.batch, "an indexer-key pool, a table row per sequence")
-    _need(u.dtype == pages.idx.dtype and u.is_contiguous() and u.shape[0] >= seqs.total_q and u.shape[1] == 128,
+    c, dt, us, (rows, cols), st = seqs.c, u.dtype, u.shape, scores.shape, scores.stride()
+    _need(pages.idx is not None and pages.batch >= c.batch, "an indexer-key pool, a table row per sequence")
+    _need(dt == pages.idx.dtype and u.is_contiguous() and us[0] >= c.total_q and us[1] == 128,
           "u: contiguous [T, 128] of the pool's type")
-    _need(scores.dtype == torch.float32 and scores.stride(1) == 1 and scores.shape[0] >= row_count
-          and scores.shape[1] >= seqs.max_seqlen_k, "scores: float32 [row_count, >= max_seqlen_k]")
-    fp8 = u.dtype == torch.uint8
-    _check(_lib.dsa_paged_scores(ctypes.byref(seqs.c), ctypes.byref(pages.c), DSA_E4M3 if fp8 else DSA_F32, _ptr(u),
-                                 _ptr(s_row), _ptr(pages.idx), _ptr(pages.idx_scale) if fp8 else None, row_begin, row_count,
-                                 _ptr(scores), scores.shape[1] if scores.shape[0] == 1 else scores.stride(0), _ptr(ws),
-                                 ws.numel(), _stream()), "dsa_paged_scores")
+    _need(scores.dtype == torch.float32 and (st[1] == 1 or cols == 1) and rows >= row_count and cols >= c.max_seqlen_k,
+          "scores: float32 [row_count, >= max_seqlen_k]")
+    fp8 = dt == torch.uint8
+    _check(_lib.dsa_paged_scores(ctypes.byref(c), ctypes.byref(pages.c), DSA_E4M3 if fp8 else DSA_F32, u.data_ptr(),
+                                 _ptr(s_row), pages.idx.data_ptr(), _ptr(pages.idx_scale) if fp8 else None, row_begin,
+                                 row_count, scores.data_ptr(), cols if rows == 1 else st[0], ws.data_ptr(), ws.numel(),
+                                 _stream()), "dsa_paged_scores")
 
 
 def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
@@ -466,10 +476,11 @@ def dsa_paged_select(seqs, pages, ia, k, idx, ws):
     """dsa_select over the paged indexer keys (ia from paged_indexer_args).  ws
     of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
     _here(idx)
-    _need(pages.table.shape[0] >= seqs.c.batch and idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
+    _need(pages.batch >= seqs.c.batch and idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
           and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k], a table row per sequence")
     _check(_lib.dsa_paged_select(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ia), k, _ptr(idx),
-                                 max(idx.stride(0), k), _ptr(ws), ws.numel(), _stream()), "dsa_paged_select")
+                                 idx.stride(0) if idx.shape[0] > 1 else idx.shape[1], _ptr(ws), ws.numel(), _stream()),
+           "dsa_paged_select")
 
 
 def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
@@ -478,13 +489,17 @@ def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
     int32 [T, >= k_sel] of local positions (-1 unused).  ws of
     dsa_workspace_size(DSA_OP_PAGED_ATTN, seqs, k_sel, None, aa) bytes."""
     _here(pages.table)
-    _need(pages.table.shape[0] >= seqs.c.batch and aa._keep[1].shape[0] >= seqs.total_q,
-          "a table row per sequence, a q row per token")
-    _need(idx is None or (idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q and idx.stride(1) == 1
-                          and idx.shape[1] >= k_sel), "idx: int32 [T, >= k_sel]")
-    _check(_lib.dsa_paged_attn(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(aa), _ptr(idx),
-                               max(idx.stride(0), k_sel) if idx is not None else 0, k_sel, _ptr(ws), ws.numel(), _stream()),
-           "dsa_paged_attn")
+    c = seqs.c
+    _need(pages.batch >= c.batch and aa._rows >= c.total_q and aa._keep[0] is pages,
+          "a table row per sequence, a q row per token, arguments over these pages")
+    ip, ld = None, 0
+    if idx is not None:
+        (rows, cols), st = idx.shape, idx.stride()
+        _need(idx.dtype == torch.int32 and rows >= c.total_q and (st[1] == 1 or cols == 1) and cols >= k_sel,
+              "idx: int32 [T, >= k_sel]")
+        ip, ld = idx.data_ptr(), st[0] if rows > 1 else max(cols, k_sel)
+    _check(_lib.dsa_paged_attn(ctypes.byref(c), ctypes.byref(pages.c), ctypes.byref(aa), ip, ld, k_sel, ws.data_ptr(),
+                               ws.numel(), _stream()), "dsa_paged_attn")
 
 
 def dsa_sync_status(ws):
