@@ -42,27 +42,38 @@ DSA_DEV void token_pos(TokenPos& tp, int64_t t, const NormRopeArgs& a) {
     tp.cs = tp.ok && ra.rope_dim ? ra.cos_sin + ri.pos * ra.rope_dim : nullptr;
 }
 
-// A lane group's walk over rows: token and head follow by addition (a 64-bit
-// division a row costs more than the row's arithmetic).
+// A lane group's walk over rows, N arrays' offsets with it: all by addition (a
+// 64-bit division a row costs more than the row's arithmetic).
+template <int N>
 struct RowWalk {
-    int64_t r, t;
+    int64_t t;
     int h;
+    int64_t off[N], head[N], wrap[N];  // elements: the row's offset; a head's; from a token's end to the next
 };
-DSA_DEV RowWalk walk_from(int64_t r, int heads) {
-    RowWalk w;
-    w.r = r;
+template <int N>
+DSA_DEV RowWalk<N> walk_from(int64_t r, int heads, const int64_t (&st)[N], const int64_t (&sh)[N]) {
+    RowWalk<N> w;
     w.t = r / heads;
     w.h = (int)(r - w.t * heads);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        w.off[i] = w.t * st[i] + w.h * sh[i];
+        w.head[i] = sh[i];
+        w.wrap[i] = st[i] - heads * sh[i];
+    }
     return w;
 }
-DSA_DEV void walk_on(RowWalk& w, int n, int heads) {
-    w.r += n;
-    if (heads == 1) {
-        w.t += n;
-        return;
-    }
+template <int N>
+DSA_DEV void walk_on(RowWalk<N>& w, int n, int heads) {
     w.h += n;
-    while (w.h >= heads) w.h -= heads, ++w.t;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w.off[i] += n * w.head[i];
+    while (w.h >= heads) {
+        w.h -= heads;
+        ++w.t;
+#pragma unroll
+        for (int i = 0; i < N; ++i) w.off[i] += w.wrap[i];
+    }
 }
 
 template <class T, int G, int NC>
@@ -73,20 +84,21 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 4 : 1) norm_rope_kernel(
     float* sm = nr_sm + (warp * RPW + sub) * a.ra.rope_dim;
     const int64_t rows = a.total_q * a.heads;
     const int64_t r0 = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp;
-    const int64_t r_end = min(rows, r0 + a.rows_per_warp);
-    RowWalk w = walk_from(r0 + sub, a.heads);
+    const int n = (int)max(min(rows - r0, a.rows_per_warp), (int64_t)0);  // rows of this warp
+    const int64_t st[2] = {a.x_stride_tok, a.y_stride_tok}, sh[2] = {a.x_stride_head, a.y_stride_head};
+    RowWalk<2> w = walk_from(r0 + sub, a.heads, st, sh);
     TokenPos tp;
     // One row at a time: many small warps hide the loads better than rows in flight
     // (a row ahead: 120 registers, 565 us for 8192 x 128 x 576 in bf16).
-    for (int64_t rr = r0; rr < r_end; rr += RPW) {
-        bool live = w.r < r_end;
+    for (int i = sub; i < n + sub; i += RPW) {
+        bool live = i < n;
         Raw8<T> cur[NC];
-        load_row<T, G, NC>(cur, (const T*)a.x + w.t * a.x_stride_tok + w.h * a.x_stride_head, a.dim, gl, live);
+        load_row<T, G, NC>(cur, (const T*)a.x + w.off[0], a.dim, gl, live);
         if (live) {
             token_pos(tp, w.t, a);
             live = tp.ok;
         }
-        row_forward<T, G, NC>(cur, (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head, a.ra, a.dim, tp.cs, gl, live, sm);
+        row_forward<T, G, NC>(cur, (T*)a.y + w.off[1], a.ra, a.dim, tp.cs, gl, live, sm);
         walk_on(w, RPW, a.heads);
     }
 }
@@ -122,14 +134,11 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
     const int64_t r0 = ((int64_t)blockIdx.x * NR_WARPS + warp) * a.rows_per_warp;
-    const int64_t r_end = min(rows, r0 + a.rows_per_warp);
-    RowWalk w = walk_from(r0 + sub, a.heads);
-    auto fetch = [&](const RowWalk& k, Raw8<T>(&rx)[NC], Raw8<T>(&rg)[NC]) {
-        load_row<T, G, NC>(rg, (const T*)a.dy + k.t * a.dy_stride_tok + k.h * a.dy_stride_head, a.dim, gl, k.r < r_end);
-        load_row<T, G, NC>(rx, (const T*)a.x + k.t * a.x_stride_tok + k.h * a.x_stride_head, n, gl, k.r < r_end);
-    };
-    // the next row is in flight while this one is worked on, where registers allow
-    constexpr bool AHEAD = NC * (int)sizeof(T) <= 8;
+    const int count = (int)max(min(rows - r0, a.rows_per_warp), (int64_t)0);  // rows of this warp
+    const int64_t st[3] = {a.x_stride_tok, a.dy_stride_tok, a.y_stride_tok};
+    const int64_t sh[3] = {a.x_stride_head, a.dy_stride_head, a.y_stride_head};
+    RowWalk<3> w = walk_from(r0 + sub, a.heads, st, sh);
+    const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
     // the weight stays in registers where they allow
     constexpr bool KEEP_W = NC <= 2;
     float wt[KEEP_W ? NC : 1][8];
@@ -141,21 +150,17 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
             for (int x = 0; x < 8; ++x) wt[i][x] = 1.f;
             if (a.ra.weight && c < n) load_weight8(a.ra.weight, c, wt[i]);
         }
-    Raw8<T> cx[NC], cg[NC];
-    if (AHEAD) fetch(w, cx, cg);
     TokenPos tp;
-    for (int64_t rr = r0; rr < r_end; rr += RPW) {
-        RowWalk nw = w;
-        walk_on(nw, RPW, a.heads);
-        Raw8<T> nx[NC], ng[NC];
-        if (AHEAD) fetch(nw, nx, ng);
-        else fetch(w, cx, cg);
-        bool live = w.r < r_end;
+    for (int i0 = sub; i0 < count + sub; i0 += RPW) {
+        bool live = i0 < count;
         if (live) {
             token_pos(tp, w.t, a);
             live = tp.ok;
         }
-        T* dx = (T*)a.y + w.t * a.y_stride_tok + w.h * a.y_stride_head;
+        Raw8<T> cx[NC], cg[NC];
+        load_row<T, G, NC>(cg, (const T*)a.dy + w.off[1], a.dim, gl, live);
+        load_row<T, G, NC>(cx, (const T*)a.x + w.off[0], n, gl, live);
+        T* dx = (T*)a.y + w.off[2];
         float g[NC][8], xv[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) unpack8(cg[i], g[i]), unpack8(cx[i], xv[i]);
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ss = fmaf(xv[i][e], xv[i][e], ss);
             ss = group_sum<G>(ss);
-            const float rstd = 1.0f / sqrtf(ss / (float)n + a.ra.eps);
+            const float rstd = live ? rsqrtf(fmaf(ss, inv_n, a.ra.eps)) : 0.f;  // no row: zeros throughout
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (gl + G * i) * 8;
@@ -178,28 +183,25 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         xv[i][e] *= rstd;  // x^
-                        if (live) acc[i][e] = fmaf(g[i][e], xv[i][e], acc[i][e]);
+                        acc[i][e] = fmaf(g[i][e], xv[i][e], acc[i][e]);
                         if (KEEP_W || a.ra.weight) g[i][e] *= wc[e];
                         dot = fmaf(g[i][e], xv[i][e], dot);
                     }
                 }
             }
-            const float k = group_sum<G>(dot) / (float)n;  // mean of g w x^
+            const float k = rstd * (group_sum<G>(dot) * inv_n);  // r times the mean of g w x^
 #pragma unroll
             for (int i = 0; i < NC; ++i)
                 if ((gl + G * i) * 8 < n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[i][e] = rstd * (g[i][e] - xv[i][e] * k);
+                    for (int e = 0; e < 8; ++e) g[i][e] = fmaf(-xv[i][e], k, rstd * g[i][e]);
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (gl + G * i) * 8;
             if (live && c < a.dim) store8(dx + c, g[i]);
         }
-        w = nw;
-        if (AHEAD)
-#pragma unroll
-            for (int i = 0; i < NC; ++i) cx[i] = nx[i], cg[i] = ng[i];
+        walk_on(w, RPW, a.heads);
     }
     if (!a.dw_part) return;
     // the block's groups, added in order; each warp's RPW row groups first

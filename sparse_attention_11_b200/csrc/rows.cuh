@@ -240,7 +240,7 @@ DSA_DEV void row_forward(const Raw8<T> (&r)[NC], T* y, const RowXform& ra, int d
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
         ss = group_sum<G>(ss);
-        const float rstd = 1.0f / sqrtf(ss / (float)ra.norm_dim + ra.eps);
+        const float rstd = rsqrtf(ss / (float)ra.norm_dim + ra.eps);  // within 2 ulp
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (gl + G * i) * 8;

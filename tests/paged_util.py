@@ -4,9 +4,9 @@ the pools the tests run them on.
 Tolerances (u = 2^-24, half a step of fp32; half a step of the output type is
 finfo.eps / 2 relative):
 * transform: fp32 arithmetic, one rounding at the end.  A norm's sum of n <= 2048
-  squares runs in chains of at most 64 terms and a tree of 5, so r is off by at
-  most (64 + 5 + 4) / 2 u; with the weight, the rotation's two products and their
-  sum 48 u of |a cos| + |b sin|.
+  squares runs in chains of at most 64 terms and a tree of 5, and the reciprocal
+  root is off by 2 ulp, so r is off by at most (64 + 5 + 2) / 2 + 4 u; with the
+  weight, the rotation's two products and their sum 48 u of |a cos| + |b sin|.
 * its gradient: the mean of g w x^ adds a chain of 64 + 5 terms of 4 roundings
   each: 160 u of r (|g w| + |x^| mean|g w x^|); d_weight: 48 u and one u per row of
   a lane's chain (at most 16 in these tests), 8 warps, 4 rows a warp: 80 u of
