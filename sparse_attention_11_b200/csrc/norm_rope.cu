@@ -150,6 +150,15 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
             for (int x = 0; x < 8; ++x) wt[i][x] = 1.f;
             if (a.ra.weight && c < n) load_weight8(a.ra.weight, c, wt[i]);
         }
+    // The next row is in flight while this one is worked on where that does not
+    // spill (heads of 128 in bf16: 51 -> 41 us; 576 columns in fp32 spill: 14 -> 21).
+    constexpr bool AHEAD = sizeof(T) == 2 ? NC <= 2 || NC == 4 : NC == 1;
+    Raw8<T> cx[NC], cg[NC];
+    auto fetch = [&](bool have) {
+        load_row<T, G, NC>(cg, (const T*)a.dy + w.off[1], a.dim, gl, have);
+        load_row<T, G, NC>(cx, (const T*)a.x + w.off[0], n, gl, have);
+    };
+    if (AHEAD) fetch(sub < count);
     TokenPos tp;
     for (int i0 = sub; i0 < count + sub; i0 += RPW) {
         bool live = i0 < count;
@@ -157,13 +166,19 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
             token_pos(tp, w.t, a);
             live = tp.ok;
         }
-        Raw8<T> cx[NC], cg[NC];
-        load_row<T, G, NC>(cg, (const T*)a.dy + w.off[1], a.dim, gl, live);
-        load_row<T, G, NC>(cx, (const T*)a.x + w.off[0], n, gl, live);
         T* dx = (T*)a.y + w.off[2];
+        if (!AHEAD) fetch(live);
         float g[NC][8], xv[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) unpack8(cg[i], g[i]), unpack8(cx[i], xv[i]);
+        if (AHEAD && !live) {  // a token without a position adds nothing, whatever its rows hold
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[i][e] = xv[i][e] = 0.f;
+        }
+        walk_on(w, RPW, a.heads);
+        if (AHEAD) fetch(i0 + RPW < count);
         if (a.ra.rope_dim > 0) rotate_chunks<G, NC>(g, a.ra, tp.cs, gl, -1.f, live, sm);
         if (n > 0) {
             float ss = 0.f, dot = 0.f;
@@ -201,7 +216,6 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
             const int c = (gl + G * i) * 8;
             if (live && c < a.dim) store8(dx + c, g[i]);
         }
-        walk_on(w, RPW, a.heads);
     }
     if (!a.dw_part) return;
     // the block's groups, added in order; each warp's RPW row groups first

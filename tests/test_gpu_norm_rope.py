@@ -148,6 +148,7 @@ def test_rows_without_a_position():
     seqs.c.total_q = 10                     # two rows behind the last sequence
     ra = row_spec(16, torch.randn(16, device="cuda"), 1e-6, 0, 16, dsa.rope_table(10, 16), True)
     x, dy = torch.randn(10, 2, 16, device="cuda"), torch.randn(10, 2, 16, device="cuda")
+    x[6:], dy[6:] = float("nan"), float("inf")
     y, dx, dw = torch.full_like(x, NOT_SET), torch.full_like(x, NOT_SET), torch.empty(16, device="cuda")
     ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_NORM_ROPE_BWD, seqs, 16))
     live = [0, 1, 2, 3, 4, 5]
