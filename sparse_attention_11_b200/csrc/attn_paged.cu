@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
     // (broadcasts tell the compiler that a value, and with it a branch or a loop, is
     // the same in all lanes: only then do the MMA operands live in uniform registers)
     const int warp = __shfl_sync(0xffffffffu, (int)warp_id(), 0), lane = (int)lane_id();
+    next_grid();
     StatusHdr* st = a.st;
     volatile int* abort = &bars->abort;
 
@@ -814,10 +815,10 @@ __global__ void __launch_bounds__(128) attn_paged_combine_kernel(const PagedAttn
     const int row = (int)(blockIdx.x - grp * (a.group * a.heads));
     PaItem it = dense ? pa_item<true>(a, grp, 0, 0) : pa_item<false>(a, grp, 0, a.k_sel);
     const int tok = row / a.heads, head = row - tok * a.heads;
-    if (tok >= it.ntok) return;
     const int64_t t = it.t0 + tok;
     const float* pl = a.part_lse + grp * a.splits * 128 + row;
     grid_wait();
+    if (tok >= it.ntok) return;
     // lane p of every warp holds the weights of parts p and p + 32
     const int lane = (int)lane_id();
     float m = -INFINITY, z[2], w[2];

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32) attn_paged_f32_kernel(const Pag
     Sm& sm = *(Sm*)pf_raw;
     constexpr int NV = DV / 32;
     const int warp = (int)warp_id(), lane = (int)lane_id();
+    next_grid();
     const int64_t t = blockIdx.x / (unsigned)a.splits;
     const int part = (int)(blockIdx.x - t * a.splits);
     const RowInfo ri = row_info_guess(a.sv, t, a.total_q);
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(PF_WARPS * 32) attn_paged_f32_kernel(const Pag
 __global__ void __launch_bounds__(128) attn_paged_f32_combine_kernel(const PagedAttnArgs a) {
     const int64_t t = blockIdx.x;
     const int lane = (int)lane_id();
-    if (!row_info_guess(a.sv, t, a.total_q).ok) return;  // left as it was
+    const bool ok = row_info_guess(a.sv, t, a.total_q).ok;
     grid_wait();
+    if (!ok) return;  // left as it was
     for (int h = (int)warp_id(); h < a.heads; h += 4) {
         // lane p holds the weights of parts p and p + 32
         float z[2], m = -INFINITY;

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
     const int lane = (int)lane_id(), gl = lane % G, sub = lane / G, warp = (int)warp_id();
     float* sm = nr_sm + (warp * RPW + sub) * a.ra.rope_dim;
     const int n = a.ra.norm_dim;
+    next_grid();
     const int64_t rows = a.total_q * a.heads;
     float acc[NC][8];
 #pragma unroll
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const 
     const int lane = (int)lane_id(), warp = (int)warp_id(), n = a.ra.norm_dim;
     const RowXform& ra = a.ra;
     const int h = ra.rope_dim >> 1;
+    next_grid();
     float* acc = nr_sm + warp * n;
     for (int c = lane; c < n; c += 32) acc[c] = 0.f;
     const int64_t rows = a.total_q * a.heads;

@@ -8,9 +8,11 @@
 namespace dsa {
 
 // ---------------------------------------------------------------------------
-// A kernel that starts while the one before it on the stream ends: it calls
-// grid_wait() before it reads what that one wrote.
+// A kernel that starts while the one before it on the stream runs (which allows
+// it by next_grid()): every block calls grid_wait(), before it reads what that one
+// wrote and in any case before it leaves.
 // ---------------------------------------------------------------------------
+DSA_DEV void next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 DSA_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class... P, class... A>
 bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {

@@ -305,6 +305,15 @@ def test_attention_f32(heads, dk, dv, own_v):
     _attn(c, heads, dk, dv, F32, kv=kv, v=v, sel=_selection(c, 40, 3, "mixed"))
 
 
+@pytest.mark.parametrize("lens", [[(1, 5000)], [(2, 12000), (1, 300)], [(1, 130), (1, 1)], [(300, 300)]])
+@pytest.mark.parametrize("heads", [1, 4, 32])
+def test_attention_f32_parts(lens, heads):
+    """One block a token, clusters of 2 to 8 parts, and more parts than a cluster."""
+    c = Cache(lens, 16)
+    _attn(c, heads, 64, 96, F32, v=c.pool(96, F32))
+    _attn(c, heads, 64, 96, F32, v=c.pool(96, F32), sel=_selection(c, 1000, 1))
+
+
 def test_attention_f32_unaligned_rows():
     c = Cache([(5, 100), (1, 33)], 7, extra_cols=3)
     _attn(c, 4, 64, 64, F32, v=c.pool(64, F32), qpad=1)
