@@ -486,7 +486,7 @@ int check_pages(const dsa_seqs* s, const dsa_pages* pg) {
     if (!pg || pg->page_size < 1 || pg->num_pages < 0) return DSA_ERR_INVALID_ARG;
     if (pg->page_size > kMaxPageSize || pg->num_pages > INT32_MAX) return DSA_ERR_UNSUPPORTED;
     if (pg->ld_table < (s->max_seqlen_k + pg->page_size - 1) / pg->page_size) return DSA_ERR_INVALID_ARG;
-    if (s->max_seqlen_k && !pg->table) return DSA_ERR_INVALID_ARG;
+    if ((s->max_seqlen_k && !pg->table) || !aligned(pg->table, 4)) return DSA_ERR_INVALID_ARG;
     return DSA_OK;
 }
 
@@ -613,7 +613,7 @@ int run_paged_scores(const dsa_seqs* s, const dsa_pages* pg, int32_t dtype, cons
 int check_idx_pool(const dsa_pages* pg, int32_t dtype, const void* k_idx, const float* k_scale) {
     if (!aligned(k_idx, 16) || !pool_ok(pg, pg->idx_page_stride, 128, 128)) return DSA_ERR_INVALID_ARG;
     if (dtype == DSA_E4M3) {
-        if (pg->num_pages && (!k_idx || !k_scale)) return DSA_ERR_INVALID_ARG;
+        if ((pg->num_pages && (!k_idx || !k_scale)) || !aligned(k_scale, 4)) return DSA_ERR_INVALID_ARG;
         if (pg->idx_page_stride % 16 || !pool_ok(pg, pg->scale_page_stride, 1, 1)) return DSA_ERR_INVALID_ARG;
     } else if (dtype == DSA_F32) {
         if (k_scale) return DSA_ERR_UNSUPPORTED;
@@ -1060,7 +1060,7 @@ int dsa_norm_rope_bwd(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtyp
     if (!r && n) r = check_rows(seqs->total_q, heads, dim, dtype, x, x_stride_tok, x_stride_head);
     if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, d_y, d_y_stride_tok, d_y_stride_head);
     if (!r) r = check_rows(seqs->total_q, heads, dim, dtype, d_x, d_x_stride_tok, d_x_stride_head);
-    if (!r && seqs->total_q && (d_x == x || d_x == d_y)) r = DSA_ERR_INVALID_ARG;
+    if (!r && ((seqs->total_q && (d_x == x || d_x == d_y)) || !aligned(d_weight, 4))) r = DSA_ERR_INVALID_ARG;
     if (!r) r = check_ws(ws, ws_bytes, norm_rope_bwd_ws(n));
     if (r) return r;
     NormRopeArgs a;
@@ -1147,7 +1147,8 @@ int dsa_paged_scores(const dsa_seqs* seqs, const dsa_pages* pages, int32_t dtype
     if (r) return r;
     if (row_begin < 0 || row_count < 0 || row_begin > seqs->total_q || row_count > seqs->total_q - row_begin)
         return DSA_ERR_INVALID_ARG;
-    if (row_count && (!u || !aligned(u, 16) || (dtype == DSA_E4M3 && !s_row))) return DSA_ERR_INVALID_ARG;
+    if (row_count && (!u || (dtype == DSA_E4M3 && !s_row))) return DSA_ERR_INVALID_ARG;
+    if (!aligned(u, 16) || !aligned(s_row, 4) || !aligned(scores, 4)) return DSA_ERR_INVALID_ARG;
     if (row_count && (!scores || ld_scores < seqs->max_seqlen_k)) return DSA_ERR_INVALID_ARG;
     r = check_ws(ws, ws_bytes, kHdr);
     if (r) return r;
@@ -1164,7 +1165,7 @@ int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_ind
     if (!r) r = check_indexer(seqs, ia);
     if (!r) r = check_idx_pool(pages, ia->dtype, ia->k_idx, ia->k_idx_scale);
     if (r) return r;
-    if (k < 1 || (seqs->total_q && (!idx || ld_idx < k))) return DSA_ERR_INVALID_ARG;
+    if (k < 1 || (seqs->total_q && (!idx || ld_idx < k)) || !aligned(idx, 4)) return DSA_ERR_INVALID_ARG;
     const PagedSelectLayout L = paged_select_layout(seqs, ia);
     r = check_ws(ws, ws_bytes, L.total);
     if (r) return r;
@@ -1195,6 +1196,7 @@ int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_
     if (seqs->total_q && (!aa->q || !aa->out || !aa->k || !aa->v)) return DSA_ERR_INVALID_ARG;
     if (!(aa->scale >= 0.f)) return DSA_ERR_INVALID_ARG;
     if (k_sel < 0 || (idx != nullptr) != (k_sel > 0) || (idx && ld_idx < k_sel)) return DSA_ERR_INVALID_ARG;
+    if (!aligned(idx, 4) || !aligned(aa->lse, 4)) return DSA_ERR_INVALID_ARG;
     const bool bf16 = aa->dtype == DSA_BF16;
     if (bf16) {
         if (aa->heads > 128 || aa->dk != 576 || aa->dv != 512 || k_sel > kTcAttnMaxSel) return DSA_ERR_UNSUPPORTED;

@@ -294,10 +294,11 @@ def _dtype(t):
     return DSA_BF16 if t.dtype == torch.bfloat16 else DSA_F32
 
 
-def _here(t):
+def _here(*tensors):
     """Refuse tensors of another device than the current one, whose stream the
     call would use."""
-    if not t.is_cuda or t.get_device() != _device():
+    dev = tensors[0].get_device()  # (-1: not a CUDA tensor)
+    if dev < 0 or dev != _device() or any(t.get_device() != dev for t in tensors):
         raise ValueError("tensors must be on the current CUDA device")
 
 
@@ -324,6 +325,9 @@ def row_args(norm_dim=0, weight=None, eps=1e-6, rope_begin=0, rope_dim=0, cos_si
     a = dsa_row_args(norm_dim, eps, weight.data_ptr() if weight is not None else None, rope_begin, rope_dim,
                      int(interleaved), cos_sin.data_ptr() if rope_dim else None, cos_sin.shape[0] if rope_dim else 0)
     a._keep = (weight, cos_sin)
+    devices = {t.device for t in (weight, cos_sin if rope_dim else None) if t is not None}
+    _need(len(devices) <= 1, "weight and cos_sin are on one device")
+    a._device = devices.pop() if devices else None
     return a
 
 
@@ -364,6 +368,10 @@ def append_args(pages, kv_new=None, kv_row=None, idx_new=None, idx_row=None):
     """Rows to append to the pools of `pages`: kv_new [T, dim] (of the KV pool's
     type) and / or idx_new [T, 128], each with its row_args or None."""
     _need(kv_new is not None or idx_new is not None, "nothing to append")
+    for t in kv_new, idx_new:
+        _need(t is None or t.device == pages.table.device, "new rows are on the pools' device")
+    for r in kv_row, idx_row:
+        _need(r is None or r._device in (None, pages.table.device), "the rows' weight and cos_sin are on the pools' device")
     a = dsa_append_args()
     a.dtype = _dtype(kv_new if kv_new is not None else idx_new)
     if kv_new is not None:
@@ -391,6 +399,7 @@ def paged_attn_args(pages, q, scale, out, lse=None):
     _need(kv is not None and q.dtype == kv.dtype and out.dtype == q.dtype, "q, out and the KV pool have one type")
     _need(q.shape[2] <= kv.shape[2] and out.shape[2] <= v.shape[2] and q.shape[:2] == out.shape[:2], "q [T,H,dk], out [T,H,dv]")
     _need(q.stride(2) == 1 and out.stride(2) == 1, "q and out: contiguous rows")
+    _need(all(t is None or t.device == kv.device for t in (q, out, lse)), "q, out and lse are on the pools' device")
     _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2]),
           "lse: contiguous float32 [T,H]")
     a = dsa_attn_args(_dtype(q), q.shape[1], q.shape[2], out.shape[2], q.data_ptr(), q.stride(0), q.stride(1),
@@ -411,7 +420,8 @@ def _rows_of(seqs, t, shape, dtype):
 def dsa_norm_rope(seqs, ra, x, y, ws):
     """y[t,h,:] = the transform ra (row_args or None) of x[t,h,:] at token t's
     position; x, y [T,H,dim] bfloat16 or float32 (y may be x)."""
-    _here(x)
+    _here(x, y, ws)
+    _need(ra is None or ra._device in (None, x.device), "weight and cos_sin are on x's device")
     sh, dt = x.shape, x.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt)
     yp, yt, yh = _rows_of(seqs, y, sh, dt)
@@ -423,7 +433,8 @@ def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
     """Backward of dsa_norm_rope: d_x [T,H,dim] (x's type) and d_weight (float32
     [norm_dim] or None) are written from x (None without a norm) and d_y.  ws of
     dsa_workspace_size(DSA_OP_NORM_ROPE_BWD, seqs, norm_dim) bytes."""
-    _here(d_y)
+    _here(*(t for t in (x, d_y, d_x, d_weight, ws) if t is not None))
+    _need(ra is None or ra._device in (None, d_y.device), "weight and cos_sin are on x's device")
     sh, dt = d_y.shape, d_y.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt) if x is not None else (None, sh[1] * sh[2], sh[2])
     gp, gt, gh = _rows_of(seqs, d_y, sh, dt)
@@ -439,7 +450,7 @@ def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
 def dsa_cache_append(seqs, pages, ap, ws):
     """Append the queries' tokens (append_args) to the paged cache at their
     positions.  seqs holds the lengths after the append."""
-    _here(pages.table)
+    _here(pages.table, ws)
     c = seqs.c
     _need(pages.batch >= c.batch, "the table has a row per sequence")
     _need(ap._rows >= c.total_q and ap._keep[0] is pages, "a row per query token, appended to these pages")
@@ -451,7 +462,9 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
     """Indexer scores of folded queries (u, s_row from dsa_fold) over the paged
     indexer keys; scores float32 [row_count, >= max_seqlen_k], -inf past a row's
     position.  dsa_topk selects from them."""
-    _here(u)
+    _here(u, scores, pages.table, ws)
+    _need(s_row is None or (s_row.device == u.device and s_row.dtype == torch.float32 and s_row.is_contiguous()
+                            and s_row.numel() >= seqs.c.total_q), "s_row: contiguous float32 [T]")
     c, dt, us, (rows, cols), st = seqs.c, u.dtype, u.shape, scores.shape, scores.stride()
     _need(pages.idx is not None and pages.batch >= c.batch, "an indexer-key pool, a table row per sequence")
     _need(dt == pages.idx.dtype and u.is_contiguous() and us[0] >= c.total_q and us[1] == 128,
@@ -475,7 +488,7 @@ def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
 def dsa_paged_select(seqs, pages, ia, k, idx, ws):
     """dsa_select over the paged indexer keys (ia from paged_indexer_args).  ws
     of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
-    _here(idx)
+    _here(idx, pages.table, ws)
     _need(pages.batch >= seqs.c.batch and idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
           and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k], a table row per sequence")
     _check(_lib.dsa_paged_select(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ia), k, _ptr(idx),
@@ -488,13 +501,14 @@ def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
     paged_attn_args): dense causal with idx None and k_sel 0, else over idx
     int32 [T, >= k_sel] of local positions (-1 unused).  ws of
     dsa_workspace_size(DSA_OP_PAGED_ATTN, seqs, k_sel, None, aa) bytes."""
-    _here(pages.table)
+    _here(pages.table, ws)
     c = seqs.c
     _need(pages.batch >= c.batch and aa._rows >= c.total_q and aa._keep[0] is pages,
           "a table row per sequence, a q row per token, arguments over these pages")
     ip, ld = None, 0
     if idx is not None:
         (rows, cols), st = idx.shape, idx.stride()
+        _here(idx)
         _need(idx.dtype == torch.int32 and rows >= c.total_q and (st[1] == 1 or cols == 1) and cols >= k_sel,
               "idx: int32 [T, >= k_sel]")
         ip, ld = idx.data_ptr(), st[0] if rows > 1 else max(cols, k_sel)

@@ -62,6 +62,7 @@ def test_norm_rope_refusals(lib):
         assert call(dtype=lib.DSA_E4M3) == U
         assert call(x=0) == I
         assert call(x=0x6001) == I
+        assert call(ws=(P(0x10000), 255, None)) == lib.DSA_ERR_WORKSPACE
         assert call(xs=(127, 64)) == I
         assert call(xs=(128, 63)) == I
         assert call(ws=(P(0x10010), 1 << 20, None)) == I
@@ -129,6 +130,8 @@ def test_scores_and_select_refusals(lib):
     assert scores(k=0) == I and scores(k=0x8004) == I and scores(ks=0) == I
     assert scores(r0=-1) == I and scores(r0=60, n=5) == I and scores(n=-1) == I
     assert scores(sc=0) == I and scores(ld=99) == I
+    assert scores(sc=0xA002) == I and scores(s_row=0x7002) == I and scores(ks=0x9002) == I
+    assert scores(_pages(lib, table=0x5002)) == I
     assert scores(_pages(lib, ld_table=6)) == I
     assert scores(ws=(P(0x10000), 64, None)) == lib.DSA_ERR_WORKSPACE
 
@@ -137,7 +140,7 @@ def test_scores_and_select_refusals(lib):
         return lib.raw_call("dsa_paged_select", ctypes.byref(_seqs(lib)), ctypes.byref(_pages(lib)), ctypes.byref(ia), k,
                             P(idx), ld, *ws)
 
-    assert select(k=0) == I and select(idx=0) == I and select(ld=7) == I
+    assert select(k=0) == I and select(idx=0) == I and select(ld=7) == I and select(idx=0xB002) == I
     assert select(scales=None) == I and select(w=None) == I and select(dtype=lib.DSA_BF16) == U
     assert select(ws=(P(0x10000), 1024, None)) == lib.DSA_ERR_WORKSPACE
 
@@ -166,7 +169,7 @@ def test_attention_refusals(lib):
     assert call(scale=-0.1) == I and call(scale=float("nan")) == I
     assert call(heads=0) == I
     assert call(k_sel=8) == I and call(idx=0xB000, ld=8) == I and call(idx=0xB000, ld=7, k_sel=8) == I
-    assert call(k_sel=-1) == I
+    assert call(k_sel=-1) == I and call(idx=0xB002, ld=8, k_sel=8) == I and call(lse=0xE002) == I
     assert call(_pages(lib, kv_page_stride=15 * 576)) == I
     assert call(ws=(P(0x10000), 128, None)) == lib.DSA_ERR_WORKSPACE
     assert call(**dict(f32, heads=33, qt=33 * 64, ot=33 * 64)) == U
@@ -235,6 +238,9 @@ def test_binding_refusals(lib):
         lambda: lib.paged_attn_args(pages, torch.zeros(3, 2, 600).bfloat16(), 1.0, torch.zeros(3, 2, 512).bfloat16()),
         lambda: lib.paged_attn_args(pages, torch.zeros(3, 2, 576).bfloat16(), 1.0, torch.zeros(3, 2, 512).bfloat16(),
                                     torch.zeros(3, 2).double()),
+        lambda: lib.dsa_norm_rope(None, None, torch.zeros(3, 2, 8), torch.zeros(3, 2, 8), torch.zeros(256)),  # CPU tensors
+        lambda: lib.dsa_cache_append(None, pages, None, torch.zeros(256)),
+        lambda: lib.dsa_paged_attn(None, pages, None, None, 0, torch.zeros(256)),
         lambda: lib.paged_indexer_args(pages, torch.zeros(3, 128), None, torch.zeros(128, 128)),
     ]
     for i, f in enumerate(bad):
