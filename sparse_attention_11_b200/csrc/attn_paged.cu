@@ -391,18 +391,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                             cp_async16_n(dst + i * PA_BLK, src[gi] + (v ? vblk(i) : kblk(i)) * 64, n[gi]);
                     }
                 };
-                got = wait_warp(smem_u32(&bars->kfree[0]), (g & 1) ^ 1, abort, st, 0x2101);
+                // (the V blocks first: their buffers are free long before the others')
+                got = wait_warp(smem_u32(&bars->vfree[s]), ((g / PA_NST) & 1) ^ 1, abort, st, 0x2104);
+                if (got) {
+                    copy(s_v + s * PA_VST, 0, 4, true);
+                    got = wait_warp(smem_u32(&bars->kfree[0]), (g & 1) ^ 1, abort, st, 0x2101);
+                }
                 if (got) {
                     copy(s_k, 0, 3, false);
                     cp_async_arrive(smem_u32(&bars->kfull));
                     got = wait_warp(smem_u32(&bars->kfree[1]), (g & 1) ^ 1, abort, st, 0x2105);
                 }
-                if (got) {
-                    copy(s_k, 3, 5, false);
-                    got = wait_warp(smem_u32(&bars->vfree[s]), ((g / PA_NST) & 1) ^ 1, abort, st, 0x2104);
-                }
                 if (!got) { ok = false; break; }
-                copy(s_v + s * PA_VST, 0, 4, true);
+                copy(s_k, 3, 5, false);
                 cp_async_arrive(smem_u32(&bars->vfull[s]));
             }
         }
