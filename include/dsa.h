@@ -409,7 +409,8 @@ DSA_API int dsa_norm_rope_bwd(const dsa_seqs* seqs, const dsa_row_args* ra, int3
  * pages that they only read.  seqs describes the lengths AFTER the new tokens:
  * cu_seqlens_k are prefix sums of the sequences' cached lengths (total_k their
  * sum) and no pool is indexed by them.  Table entries past a sequence's last
- * page are not read.  A position whose entry is not in [0, num_pages) is
+ * page are not read.  Calls that may run at the same time (on other streams, in
+ * graphs replayed together) need workspaces of their own.  A position whose entry is not in [0, num_pages) is
  * recorded as DSA_ERR_INDEX and touches no memory.                           */
 typedef struct dsa_pages {
     int32_t page_size;
@@ -467,7 +468,8 @@ DSA_API int dsa_paged_scores(const dsa_seqs* seqs, const dsa_pages* pages, int32
 
 /* dsa_select over the paged indexer keys: ia->k_idx and ia->k_idx_scale are
  * the pools.  The scores pass through the workspace (DSA_OP_PAGED_SELECT), at
- * most 1 GiB of them at a time (or one row's, where that is more). */
+ * most 1 GiB of them at a time (or one row's, where that is more).  A position
+ * without a valid page scores 0 here and is recorded. */
 DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_indexer_args* ia, int32_t k,
                              int32_t* idx, int64_t ld_idx, void* ws, size_t ws_bytes, dsa_stream_t stream);
 
@@ -475,8 +477,8 @@ DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const
  * with aa->k (and aa->v) the pools and k_stride the row stride inside a page.
  * idx NULL (k_sel 0): dense causal, keys 0..pos.  Else query t attends to the
  * valid slots j < k_sel of idx row t (local positions, as dsa_paged_select
- * leaves them; -1 unused).  A row with nothing to attend to gives out = 0 and
- * lse = -inf.  Slots with an index >= seqlen_k(b) or without a valid page are
+ * leaves them, in any order; -1 unused; a position listed twice counts twice).
+ * A row with nothing to attend to gives out = 0 and lse = -inf.  Slots with an index >= seqlen_k(b) or without a valid page are
  * skipped and recorded; so are, in the fp32 dense form, positions without a
  * valid page (in the bf16 dense form such a position counts as a row of zeros).
  * A token whose position is invalid is recorded, and its rows (where tokens are

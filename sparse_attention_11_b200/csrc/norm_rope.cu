@@ -14,7 +14,9 @@
 // Both are bound by HBM: a row is read once and written once (backward: x and
 // dy once, dx once); a group of 8 lanes (dim <= 256) or 32 lanes holds a row in
 // registers as 16-byte chunks, so the norm's reduction and the rotation need
-// no second read.  All arithmetic is fp32; the result is rounded once.
+// no second read.  All arithmetic is fp32; the result is rounded once.  8192 x 128
+// rows of 576 in bf16: 427 us, 0.87 of the copy bandwidth; the backward of 236K
+// rows of 128 in bf16: 41 us, 0.68 (16 warps an SM at 128 registers).
 //
 // dw is summed in a fixed order, whatever the launch: each lane sums its
 // columns over its block's rows, the block's groups are added in order, and a

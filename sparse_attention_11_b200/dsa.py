@@ -356,12 +356,18 @@ class Pages:
         _need(idx_scale is None or (idx_scale.dim() == 2 and idx_scale.dtype == torch.float32
                                     and (idx_scale.stride(1) == 1 or size == 1)), "idx_scale: float32 [pages, page_size]")
         self.table, self.kv, self.v, self.idx, self.idx_scale = table, kv, v, idx, idx_scale
-        self.batch = table.shape[0]
+        self.batch, self.positions = table.shape[0], table.shape[1] * size
 
         def page(p):
             return 0 if p is None else p.stride(0)
 
-        self.c = dsa_pages(size, n, table.data_ptr(), table.stride(0), page(kv), page(v), page(idx), page(idx_scale))
+        self.c = dsa_pages(size, n, table.data_ptr(), max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else
+                           table.stride(0), page(kv), page(v), page(idx), page(idx_scale))
+
+    def need(self, c):
+        """Refuse a batch (a dsa_seqs) that the table does not hold."""
+        if self.batch < c.batch or self.positions < c.max_seqlen_k:
+            raise ValueError("the table has a row per sequence and an entry per page of the longest")
 
 
 def append_args(pages, kv_new=None, kv_row=None, idx_new=None, idx_row=None):
@@ -452,7 +458,7 @@ def dsa_cache_append(seqs, pages, ap, ws):
     positions.  seqs holds the lengths after the append."""
     _here(pages.table, ws)
     c = seqs.c
-    _need(pages.batch >= c.batch, "the table has a row per sequence")
+    pages.need(c)
     _need(ap._rows >= c.total_q and ap._keep[0] is pages, "a row per query token, appended to these pages")
     _check(_lib.dsa_cache_append(ctypes.byref(c), ctypes.byref(pages.c), ctypes.byref(ap), ws.data_ptr(), ws.numel(),
                                  _stream()), "dsa_cache_append")
@@ -466,7 +472,8 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
     _need(s_row is None or (s_row.device == u.device and s_row.dtype == torch.float32 and s_row.is_contiguous()
                             and s_row.numel() >= seqs.c.total_q), "s_row: contiguous float32 [T]")
     c, dt, us, (rows, cols), st = seqs.c, u.dtype, u.shape, scores.shape, scores.stride()
-    _need(pages.idx is not None and pages.batch >= c.batch, "an indexer-key pool, a table row per sequence")
+    pages.need(c)
+    _need(pages.idx is not None, "an indexer-key pool")
     _need(dt == pages.idx.dtype and u.is_contiguous() and us[0] >= c.total_q and us[1] == 128,
           "u: contiguous [T, 128] of the pool's type")
     _need(scores.dtype == torch.float32 and (st[1] == 1 or cols == 1) and rows >= row_count and cols >= c.max_seqlen_k,
@@ -489,8 +496,9 @@ def dsa_paged_select(seqs, pages, ia, k, idx, ws):
     """dsa_select over the paged indexer keys (ia from paged_indexer_args).  ws
     of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
     _here(idx, pages.table, ws)
-    _need(pages.batch >= seqs.c.batch and idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
-          and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k], a table row per sequence")
+    pages.need(seqs.c)
+    _need(idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
+          and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k]")
     _check(_lib.dsa_paged_select(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ia), k, _ptr(idx),
                                  idx.stride(0) if idx.shape[0] > 1 else idx.shape[1], _ptr(ws), ws.numel(), _stream()),
            "dsa_paged_select")
@@ -503,8 +511,8 @@ def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
     dsa_workspace_size(DSA_OP_PAGED_ATTN, seqs, k_sel, None, aa) bytes."""
     _here(pages.table, ws)
     c = seqs.c
-    _need(pages.batch >= c.batch and aa._rows >= c.total_q and aa._keep[0] is pages,
-          "a table row per sequence, a q row per token, arguments over these pages")
+    pages.need(c)
+    _need(aa._rows >= c.total_q and aa._keep[0] is pages, "a q row per token, arguments over these pages")
     ip, ld = None, 0
     if idx is not None:
         (rows, cols), st = idx.shape, idx.stride()

@@ -447,6 +447,38 @@ class Layer:
         dsa.dsa_paged_attn(s, self.pages, p["aa"], x["idx"], self.k, ws)
 
 
+def test_binding_refusals():
+    """What the binding can see of a call that would read or write out of range."""
+    c = Cache([(2, 100), (1, 40)], 16)
+    dsa = c.dsa
+    kv = c.pool(576, BF)
+    q, out = c.randn(3, 128, 576, dtype=BF), torch.empty(3, 128, 512, dtype=BF, device="cuda")
+    ws = dsa.workspace(1 << 26)
+
+    def attn(table=c.table, q=q, idx=None, k=0, ws=ws):
+        pages = dsa.Pages(table, kv=kv)
+        dsa.dsa_paged_attn(c.seqs, pages, dsa.paged_attn_args(pages, q, 0.1, out[:len(q)]), idx, k, ws)
+
+    attn()
+    sel = torch.zeros(3, 8, dtype=torch.int32, device="cuda")
+    bad = [lambda: attn(table=c.table[:, :6]), lambda: attn(table=c.table[:1]), lambda: attn(q=q[:2]),
+           lambda: attn(idx=sel, k=9), lambda: attn(idx=sel[:2], k=8), lambda: attn(idx=sel.long(), k=8),
+           lambda: attn(idx=sel.cpu(), k=8), lambda: attn(ws=ws.cpu()),
+           lambda: dsa.paged_attn_args(dsa.Pages(c.table, kv=kv), q.cpu(), 0.1, out),
+           lambda: dsa.append_args(dsa.Pages(c.table, kv=kv), kv_new=torch.zeros(3, 576, dtype=BF)),
+           lambda: dsa.append_args(dsa.Pages(c.table, kv=kv), kv_new=q[:, 0],
+                                   kv_row=dsa.row_args(norm_dim=8, weight=torch.ones(8))),
+           lambda: dsa.dsa_norm_rope(c.seqs, dsa.row_args(norm_dim=8, weight=torch.ones(8)), q, torch.empty_like(q), ws),
+           lambda: dsa.dsa_norm_rope(c.seqs, None, q, torch.empty_like(q)[:2], ws)]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, dsa.DsaError)):
+            f()
+            pytest.fail(f"accepted: {i}")
+    with pytest.raises(dsa.DsaError):
+        attn(ws=ws[:128])
+    dsa.check_device_status(ws)
+
+
 def _prefix(lens):
     return np.concatenate([[0], np.cumsum(lens)])
 
