@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         mbar_init(smem_u32(&bars->s_free), 8);
         mbar_init(smem_u32(&bars->p_full), 8);
         mbar_init(smem_u32(&bars->p_free), 1);
-        mbar_init(smem_u32(&bars->q_full), 4);
+        mbar_init(smem_u32(&bars->q_full), 8);
         mbar_init(smem_u32(&bars->q_free), 1);
         mbar_init(smem_u32(&bars->o_full), 1);
         mbar_init(smem_u32(&bars->o_free), 4);
@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
     // item are zero.  Loads take 4 rows x 128 bytes an instruction: a row a lane
     // costs 32 cache lines each (9200 cycles an item, now about 2500).
     // wait: until the last S of the item before has completed
-    auto load_q = [&](const PaItem& it, int quad, uint8_t* stg, auto wait) -> bool {
+    // part: of two warps that share the rows, the first or the second half of the
+    // blocks; 2: all.
+    auto load_q = [&](const PaItem& it, int quad, uint8_t* stg, int part, auto wait) -> bool {
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const int sub = lane >> 3, chunk = lane & 7;
         int64_t off[8];  // rows 4 j + sub of this warp
@@ -276,22 +278,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                 x[j] = off[j] >= 0 ? __ldg((const uint4*)(q + off[j] + blk * 64)) : make_uint4(0u, 0u, 0u, 0u);
         };
         auto blk_of = [&](int i) { return i < 2 ? kblk(3 + i) : vblk(i - 2); };  // tensor-memory blocks in their order
-        fetch(blk_of(0));
+        const int i0 = part == 1 ? 3 : 0, i1 = part == 0 ? 3 : 6;
+        fetch(blk_of(i0));
         if (!wait()) return false;
         tc_fence_after();
         const uint32_t sq = smem_u32(smem + Lay::OFF_Q);
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
+#pragma unroll 1
+        for (int i = part == 1 ? 2 : 0; i < (part == 0 ? 2 : 3); ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 cp_async16_n(sq + i * PA_QBLK + pa_swz(quad * 32 + 4 * j + sub, chunk),
                              q + (off[j] >= 0 ? off[j] + kblk(i) * 64 : 0), off[j] >= 0 ? 16u : 0u);
 #pragma unroll 1
-        for (int i = 0; i < 6; ++i) {
+        for (int i = i0; i < i1; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) *(uint4*)(stg + pa_swz(4 * j + sub, chunk)) = x[j];
             __syncwarp();
-            if (i < 5) fetch(blk_of(i + 1));
+            if (i + 1 < i1) fetch(blk_of(i + 1));
             uint32_t r[32];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -521,12 +524,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         float* xm = (float*)(smem + Lay::OFF_XM);
         uint32_t g = 0, e = 0;
         bool ok = true;
-        // the first item's Q, while the epilogue warps read its selection (staged in
-        // P's buffer; not used if the item turns out empty)
-        if (kh == 0 && nq > 0) {
+        // the first item's Q, half of its blocks a warp, while the epilogue warps read
+        // its selection (staged in P's buffer and theirs; not used if the item turns out
+        // empty)
+        if (nq > 0) {
             const int64_t grp = item0 / a.splits;
-            load_q(pa_item<DENSE>(a, grp, (int)(item0 - grp * a.splits), sel_part), quad, smem + Lay::OFF_P + quad * 4096,
-                   [] { return true; });
+            load_q(pa_item<DENSE>(a, grp, (int)(item0 - grp * a.splits), sel_part), quad,
+                   smem + (kh == 0 ? Lay::OFF_P : Lay::OFF_EPI) + quad * 4096, kh, [] { return true; });
             if (!info_wait(0, 0x2301)) ok = false;
             else if (tiles_of(0) > 0 && lane == 0) mbar_arrive(smem_u32(&bars->q_full));
             __syncwarp();
@@ -784,8 +788,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                     if (e > 0) return wait_warp(smem_u32(&bars->q_free), (e - 1) & 1, abort, st, 0x2404);
                     return qi > 1 || wait_warp(smem_u32(&bars->info_empty[0]), 0, abort, st, 0x2405);
                 };
-                if (!load_q(it, quad, stg, wait)) { ok = false; break; }
-                if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+                if (!load_q(it, quad, stg, 2, wait)) { ok = false; break; }
+                if (lane < 2) mbar_arrive(smem_u32(&bars->q_full));  // (for two warps of the first)
             }
             // ---- the previous item's epilogue (this item's first S overlaps it) ----
             if (pend && !epilogue(it_pend, item_pend, e - 1)) { ok = false; break; }
