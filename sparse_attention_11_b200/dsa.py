@@ -289,17 +289,25 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+_DTYPES = {torch.bfloat16: DSA_BF16, torch.float32: DSA_F32}
+
+
 def _dtype(t):
-    _need(t.dtype in (torch.bfloat16, torch.float32), "bfloat16 or float32 expected")
-    return DSA_BF16 if t.dtype == torch.bfloat16 else DSA_F32
+    _need(t.dtype in _DTYPES, "bfloat16 or float32 expected")
+    return _DTYPES[t.dtype]
 
 
 def _here(*tensors):
     """Refuse tensors of another device than the current one, whose stream the
     call would use."""
     dev = tensors[0].get_device()  # (-1: not a CUDA tensor)
-    if dev < 0 or dev != _device() or any(t.get_device() != dev for t in tensors):
-        raise ValueError("tensors must be on the current CUDA device")
+    if dev >= 0 and dev == _device():
+        for t in tensors:
+            if t.get_device() != dev:
+                break
+        else:
+            return dev
+    raise ValueError("tensors must be on the current CUDA device")
 
 
 def rope_table(positions, dim, base=10000.0, device="cuda"):
@@ -328,6 +336,7 @@ def row_args(norm_dim=0, weight=None, eps=1e-6, rope_begin=0, rope_dim=0, cos_si
     devices = {t.device for t in (weight, cos_sin if rope_dim else None) if t is not None}
     _need(len(devices) <= 1, "weight and cos_sin are on one device")
     a._device = devices.pop() if devices else None
+    a._index = (weight if weight is not None else cos_sin).get_device() if a._device is not None else None
     return a
 
 
@@ -420,27 +429,30 @@ def _rows_of(seqs, t, shape, dtype):
     s = t.stride()
     if t.shape != shape or len(s) != 3 or shape[0] < seqs.c.total_q or (s[2] != 1 and shape[2] > 1) or t.dtype != dtype:
         raise ValueError("rows: [T, heads, dim] of one shape and type, contiguous columns")
-    return t.data_ptr(), s[0], s[1]
+    # (a dimension of one has any stride)
+    return t.data_ptr(), s[0] if shape[0] > 1 else max(s[0], shape[1] * max(s[1], shape[2])), \
+        s[1] if shape[1] > 1 else max(s[1], shape[2])
 
 
 def dsa_norm_rope(seqs, ra, x, y, ws):
     """y[t,h,:] = the transform ra (row_args or None) of x[t,h,:] at token t's
     position; x, y [T,H,dim] bfloat16 or float32 (y may be x)."""
-    _here(x, y, ws)
-    _need(ra is None or ra._device in (None, x.device), "weight and cos_sin are on x's device")
+    dev = _here(x, y, ws)
+    _need(ra is None or ra._index is None or ra._index == dev, "weight and cos_sin are on x's device")
     sh, dt = x.shape, x.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt)
     yp, yt, yh = _rows_of(seqs, y, sh, dt)
-    _check(_lib.dsa_norm_rope(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(x), sh[1], sh[2],
-                              xp, xt, xh, yp, yt, yh, ws.data_ptr(), ws.numel(), _stream()), "dsa_norm_rope")
+    _check(_lib.dsa_norm_rope(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _DTYPES.get(dt, -1),
+                              sh[1], sh[2], xp, xt, xh, yp, yt, yh, ws.data_ptr(), ws.numel(), _stream()),
+           "dsa_norm_rope")
 
 
 def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
     """Backward of dsa_norm_rope: d_x [T,H,dim] (x's type) and d_weight (float32
     [norm_dim] or None) are written from x (None without a norm) and d_y.  ws of
     dsa_workspace_size(DSA_OP_NORM_ROPE_BWD, seqs, norm_dim) bytes."""
-    _here(*(t for t in (x, d_y, d_x, d_weight, ws) if t is not None))
-    _need(ra is None or ra._device in (None, d_y.device), "weight and cos_sin are on x's device")
+    dev = _here(*[t for t in (x, d_y, d_x, d_weight, ws) if t is not None])
+    _need(ra is None or ra._index is None or ra._index == dev, "weight and cos_sin are on x's device")
     sh, dt = d_y.shape, d_y.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt) if x is not None else (None, sh[1] * sh[2], sh[2])
     gp, gt, gh = _rows_of(seqs, d_y, sh, dt)
@@ -448,7 +460,7 @@ def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
     _need(d_weight is None or (d_weight.dtype == torch.float32 and d_weight.is_contiguous()
                                and d_weight.numel() == (ra.norm_dim if ra is not None else 0)),
           "d_weight: contiguous float32 [norm_dim]")
-    _check(_lib.dsa_norm_rope_bwd(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _dtype(d_y),
+    _check(_lib.dsa_norm_rope_bwd(ctypes.byref(seqs.c), ctypes.byref(ra) if ra is not None else None, _DTYPES.get(dt, -1),
                                   sh[1], sh[2], xp, xt, xh, gp, gt, gh, dp, dt_, dh, _ptr(d_weight), ws.data_ptr(),
                                   ws.numel(), _stream()), "dsa_norm_rope_bwd")
 
