@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(PF_WARPS * 32) attn_paged_f32_kernel(const Pag
                 for (int x = 0; x < NV; ++x) o[i][x] *= c;
                 m[i] = mt;
             }
-            const float p = ok && m[i] != -INFINITY ? expf(z - m[i]) : 0.f;
+            // (a score of -inf adds nothing, also while there is no maximum; a NaN stays NaN)
+            const float p = z == -INFINITY ? 0.f : expf(z - m[i]);
             float ps = p;
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);

@@ -353,6 +353,39 @@ def test_attention_bad_slots(dtype):
     _attn(c, H, dk, dv, dtype, kv=kv, sel=sel, status=c.dsa.DSA_ERR_INDEX)
 
 
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_nan_query(dtype, selected):
+    """A query row of NaN gives a row of NaN and a NaN lse, its neighbours what
+    they give without it; a row of a selection with no valid slot gives zeros."""
+    c = Cache([(3, 200), (2, 60)], 16)
+    dsa = c.dsa
+    H, dk, dv = (128, 576, 512) if dtype == BF else (4, 64, 64)
+    kv, q = c.pool(dk, dtype), c.randn(c.T, H, dk, dtype=dtype)
+    sel = torch.arange(40, dtype=torch.int32, device="cuda").repeat(c.T, 1) if selected else None
+    if selected:
+        sel[3] = -1
+    pages = dsa.Pages(c.table, kv=kv)
+    got = []
+    for bad in (False, True):
+        if bad:
+            q[1, 2], q[3, 0] = float("nan"), float("nan")
+        out, lse = torch.empty(c.T, H, dv, dtype=dtype, device="cuda"), torch.empty(c.T, H, device="cuda")
+        aa = dsa.paged_attn_args(pages, q, 0.1, out, lse)
+        k = sel.shape[1] if selected else 0
+        ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_PAGED_ATTN, c.seqs, k, None, aa))
+        dsa.dsa_paged_attn(c.seqs, pages, aa, sel, k, ws)
+        dsa.check_device_status(ws)
+        got.append((out, lse))
+    (o0, l0), (o1, l1) = got
+    nan = torch.zeros(c.T, H, dtype=torch.bool, device="cuda")
+    nan[1, 2], nan[3, 0] = True, not selected
+    assert torch.equal(torch.isnan(l1), nan) and torch.equal(torch.isnan(o1).all(-1), nan)
+    assert torch.equal(o1[~nan], o0[~nan]) and torch.equal(l1[~nan], l0[~nan])
+    if selected:
+        assert bool((o1[3] == 0).all()) and bool((l1[3] == -float("inf")).all())
+
+
 def test_attention_without_lse():
     c = Cache([(3, 100)], 16)
     _attn(c, 128, 576, 512, BF, lse=False)
