@@ -375,7 +375,9 @@ typedef struct dsa_row_args {
 
 /* y[t, h, :] = the transform of x[t, h, :] at token t's position (seqs rule),
  * for heads rows a token (heads = 1 for the shared KV row).  dtype (x and y):
- * DSA_BF16 or DSA_F32.  y may be x (same strides).  ra NULL: a copy.  A token
+ * DSA_BF16 or DSA_F32.  A token's rows lie together: stride_head >= dim and
+ * stride_tok >= (heads - 1) * stride_head + dim (dsa_paged_attn's q and out
+ * too); other layouts are refused.  y may be x (same strides).  ra NULL: a copy.  A token
  * whose position is invalid or >= rope_positions is recorded as DSA_ERR_INDEX
  * and its rows are left as they were.  Workspace: a status header. */
 DSA_API int dsa_norm_rope(const dsa_seqs* seqs, const dsa_row_args* ra, int32_t dtype, int32_t heads, int32_t dim,

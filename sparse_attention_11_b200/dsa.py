@@ -500,6 +500,8 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
 def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
     """indexer_args over the indexer-key pool of `pages`."""
     _need(pages.idx is not None and pages.idx.dtype == q_idx.dtype, "q_idx has the indexer-key pool's type")
+    _need(all(t is None or t.device == pages.idx.device for t in (q_idx, q_idx_scale, w_index, k_per_row)),
+          "queries, weights and k_per_row are on the pools' device")
     return indexer_args(q_idx, q_idx_scale, w_index, pages.idx, pages.idx_scale if q_idx.dtype == torch.uint8 else None,
                         k_per_row)
 
@@ -509,6 +511,10 @@ def dsa_paged_select(seqs, pages, ia, k, idx, ws):
     of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
     _here(idx, pages.table, ws)
     pages.need(seqs.c)
+    _need(pages.idx is not None and (ia.k_idx or 0) == pages.idx.data_ptr()
+          and (not ia.k_idx_scale or (pages.idx_scale is not None and ia.k_idx_scale == pages.idx_scale.data_ptr())),
+          "arguments over these pages")
+    _need(ia._keep[0].shape[0] >= seqs.total_q, "a q_idx row per query token")
     _need(idx.dtype == torch.int32 and idx.shape[0] >= seqs.total_q
           and idx.shape[1] >= k and idx.stride(1) == 1, "idx: int32 [T, >= k]")
     _check(_lib.dsa_paged_select(ctypes.byref(seqs.c), ctypes.byref(pages.c), ctypes.byref(ia), k, _ptr(idx),

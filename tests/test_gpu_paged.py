@@ -512,6 +512,34 @@ def test_binding_refusals():
     dsa.check_device_status(ws)
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+def test_select_binding_refusals(fp8):
+    """Arguments made over other pools, fewer queries than the batch, another device."""
+    c = Cache([(2, 100), (1, 40)], 16)
+    dsa = c.dsa
+    idx, sc = c.key_pool(fp8)
+    pages, other = dsa.Pages(c.table, idx=idx, idx_scale=sc), None
+    if fp8:
+        q, qs = torch.zeros(3, 128, dtype=torch.uint8, device="cuda"), torch.ones(3, device="cuda")
+        w = torch.ones(128, 128, dtype=BF, device="cuda")
+        other = dsa.Pages(c.table, idx=idx, idx_scale=sc.clone())
+    else:
+        q, qs, w = torch.zeros(3, 128, device="cuda"), None, torch.ones(128, 128, device="cuda")
+    short = dsa.Pages(c.table, idx=idx[:4].clone(), idx_scale=None if sc is None else sc[:4].clone())
+    out = torch.empty(3, 8, dtype=torch.int32, device="cuda")
+    ia = dsa.paged_indexer_args(pages, q, qs, w)
+    ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_PAGED_SELECT, c.seqs, 8, ia))
+    bad = [lambda: dsa.dsa_paged_select(c.seqs, pages, dsa.paged_indexer_args(short, q, qs, w), 8, out, ws),
+           lambda: dsa.dsa_paged_select(c.seqs, pages, dsa.paged_indexer_args(pages, q[:2], qs, w), 8, out, ws),
+           lambda: dsa.paged_indexer_args(pages, q.cpu(), qs, w), lambda: dsa.paged_indexer_args(pages, q, qs, w.cpu())]
+    if other is not None:
+        bad.append(lambda: dsa.dsa_paged_select(c.seqs, other, ia, 8, out, ws))
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"accepted: {i}")
+
+
 def _prefix(lens):
     return np.concatenate([[0], np.cumsum(lens)])
 
