@@ -93,7 +93,7 @@ struct PaBars {
     uint64_t q_full, q_free;    // Q in place / its last S complete
     uint64_t o_full, o_free;    // O complete / read by the epilogue
     uint64_t xm_full[4];        // a tile's maxima of both key halves, per lane quadrant
-    uint64_t ml_full;           // an item's maxima and sums
+    uint64_t ml_full[2];        // an item's maxima and sums, per ring slot
     uint64_t info_full[2], info_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         mbar_init(smem_u32(&bars->q_free), 1);
         mbar_init(smem_u32(&bars->o_full), 1);
         mbar_init(smem_u32(&bars->o_free), 4);
-        mbar_init(smem_u32(&bars->ml_full), 8);
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->xm_full[i]), 2);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->ml_full[i]), 8);
             mbar_init(smem_u32(&bars->info_full[i]), 4);
             mbar_init(smem_u32(&bars->info_empty[i]), 9 + PA_PRODUCERS);  // 8 softmax warps, the MMA warp, the producers
         }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             if (kh == 0) ml[h] = m_used;
             ml[128 + kh * 128 + h] = l;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->ml_full));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->ml_full[e & 1]));
             ++e;
         }
     } else {
@@ -656,7 +656,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         // Rows leave through this warp's staging tile, so that a store covers
         // 64-byte pieces of 8 rows.
         auto epilogue = [&](const PaItem& it, int64_t item, uint32_t e) -> bool {
-            if (!wait_warp(smem_u32(&bars->ml_full), e & 1, abort, st, 0x2401)) return false;
+            // (a barrier for each slot of the ring: item e + 1 may finish its softmax before
+            // this warp looks, item e + 2 not before this epilogue has read O)
+            if (!wait_warp(smem_u32(&bars->ml_full[e & 1]), (e >> 1) & 1, abort, st, 0x2401)) return false;
             const float* ml = (const float*)(smem + Lay::OFF_ML) + (e & 1) * 384;
             const float m_used = ml[h], l = ml[128 + h] + ml[256 + h];
             const float inv = l != 0.f ? 1.0f / l : 0.f;  // a NaN sum stays a NaN row
