@@ -774,6 +774,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             __syncwarp();
             return true;
         };
+        // (groups are cut from the sequences: a token of none falls in no group)
+        if (DENSE && a.group > 1 && blockIdx.x == 0 && threadIdx.x == 32 * PA_EPI0)
+            report_no_sequence(a.sv, 0, a.total_q, st);
         uint32_t e = 0;     // items with tiles begun
         bool ok = nq == 0 || publish(0), pend = false;  // the (e - 1)-th item's epilogue is still to be done
         int64_t item_pend = 0;

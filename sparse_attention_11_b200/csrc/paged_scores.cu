@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(PsSmem<NQ>::THREADS) paged_scores_kernel(const
     const int warp = (int)warp_id(), lane = (int)lane_id();
     volatile int* abort = &bars->abort;
     StatusHdr* st = a.st;
+    if (blockIdx.x == 0 && threadIdx.x == 0) report_no_sequence(a.sv, a.row_begin, a.row_begin + a.row_count, st);
 
     // this CTA: queries [t_first, t_first + nrows) of sequence b, key tiles [t_lo, t_hi)
     const int64_t nblk = (a.max_seqlen_q + NQ - 1) / NQ;
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(PFW_THREADS) paged_scores_few_kernel(const Pag
     StatusHdr* st = a.st;
     const int64_t tiles = (a.cols + PS_KEYS - 1) / PS_KEYS;
     const int batch = a.sv.batch;
+    if (blockIdx.x == 0 && threadIdx.x == 32 * PFW_MMA - 1) report_no_sequence(a.sv, a.row_begin, a.row_begin + a.row_count, st);
     if (threadIdx.x == 0) {
         for (int i = 0; i < PS_NST; ++i) {
             mbar_init(smem_u32(&bars->full[i]), PS_PROD * 32);

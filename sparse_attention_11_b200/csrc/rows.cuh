@@ -43,6 +43,14 @@ DSA_DEV RowInfo row_info_guess(const SeqView& sv, int64_t t, int64_t total_q) {
     return r;
 }
 
+// Records the first of the tokens [first, end) that no sequence holds, for kernels
+// that walk over sequences and would pass it by.
+DSA_DEV void report_no_sequence(const SeqView& sv, int64_t first, int64_t end, StatusHdr* st) {
+    const int64_t lo = __ldg(sv.cu_q), hi = __ldg(sv.cu_q + sv.batch);
+    if (first < min(lo, end)) report(st, DSA_ERR_INDEX, first);
+    else if (end > max(hi, first)) report(st, DSA_ERR_INDEX, max(hi, first));
+}
+
 // ---------------------------------------------------------------------------
 // Page table: the pool row of a sequence's position.
 // ---------------------------------------------------------------------------

@@ -50,3 +50,45 @@ def test_attention_bf16_items_of_one_tile(heads, selected):
     assert_attention(c, *got[0], attention(c, q, kv, kv[..., :512], scale, sel), BF)
     for o, l in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+
+
+# ----------------------------------------------------------------------------- tokens of no sequence
+@pytest.mark.parametrize("heads", [128, 64, 16, 1])
+def test_attention_dense_token_behind_the_last_sequence(heads):
+    """Recorded, its rows left as they were, where tokens are handled in groups too."""
+    c = Cache([(2, 50), (3, 70)], 16)
+    c.seqs.c.total_q, c.T = 7, 7
+    aa, q, out, lse, ws, pages, scale = _plan(c, c.pool(576, BF), heads, 576, 512, BF)
+    c.dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+    code, token = c.dsa.dsa_sync_status(ws)
+    assert code == c.dsa.DSA_ERR_INDEX and token in (5, 6)
+    assert bool((out[5:] == NOT_SET).all()) and bool((lse[5:] == NOT_SET).all())
+    c.T = 5
+    assert_attention(c, out[:5], lse[:5], attention(c, q[:5], pages.kv, pages.kv[..., :512], scale), BF)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("lens", [[(1, 300), (2, 40)], [(40, 300), (2, 40)]])
+def test_scores_token_behind_the_last_sequence(fp8, lens):
+    """At most 16 queries a sequence and more: recorded where its row is asked for."""
+    c = Cache(lens, 32)
+    dsa, n = c.dsa, c.T
+    k, sc = c.key_pool(fp8)
+    u = c.randn(n + 2, 128)
+    if fp8:
+        u = u.to(torch.float8_e4m3fn).view(torch.uint8)
+    s_row = torch.ones(n + 2, device="cuda")
+    c.seqs.c.total_q = n + 2
+    pages = dsa.Pages(c.table, idx=k, idx_scale=sc)
+    ws = dsa.workspace(256)
+    got = torch.full((n + 2, 300), NOT_SET, device="cuda")
+    dsa.dsa_paged_scores(c.seqs, pages, u, s_row, 0, n, got, ws)
+    assert dsa.dsa_sync_status(ws)[0] == dsa.DSA_OK
+    first = got.clone()
+    dsa.dsa_paged_scores(c.seqs, pages, u, s_row, 1, n, got[1:], ws)
+    code, token = dsa.dsa_sync_status(ws)
+    assert code == dsa.DSA_ERR_INDEX and token == n
+    assert torch.equal(got, first) and bool((got[n:] == NOT_SET).all())
+    dsa.dsa_paged_scores(c.seqs, pages, u, s_row, 0, n + 2, got, ws)
+    assert dsa.dsa_sync_status(ws)[0] == dsa.DSA_ERR_INDEX
+    assert bool((got[n:] == NOT_SET).all())
