@@ -480,9 +480,9 @@ DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const
  * idx NULL (k_sel 0): dense causal, keys 0..pos.  Else query t attends to the
  * valid slots j < k_sel of idx row t (local positions, as dsa_paged_select
  * leaves them, in any order; -1 unused; a position listed twice counts twice).
- * A row with nothing to attend to gives out = 0 and lse = -inf.  Slots with an index >= seqlen_k(b) or without a valid page are
- * skipped and recorded; so are, in the fp32 dense form, positions without a
- * valid page (in the bf16 dense form such a position counts as a row of zeros).
+ * A row with nothing to attend to gives out = 0 and lse = -inf.  Slots with an
+ * index >= seqlen_k(b), and slots and positions without a valid page, are skipped
+ * and recorded.
  * A token whose position is invalid is recorded, and its rows (where tokens are
  * handled together, theirs too) are left as they were.
  * Supported: DSA_BF16 with heads <= 128, dk = 576, dv = 512, v = k (V the

@@ -78,7 +78,7 @@ struct PaLayout {
     static constexpr uint32_t OFF_XM = OFF_ML + 2 * 1536;        // [2][2][128] the key halves' maxima of a tile
     static constexpr uint32_t OFF_VM = OFF_XM + 2 * 1024;        // [2][64] validity bits of 2048 slots
     static constexpr uint32_t OFF_ITEM = OFF_VM + 512;           // [2] PaItem
-    static constexpr uint32_t OFF_INFO = OFF_ITEM + 128;         // [2][8] last used slot per epilogue warp
+    static constexpr uint32_t OFF_INFO = OFF_ITEM + 128;         // [2][8] per epilogue warp: last used slot, (dense) pages missing
     static constexpr uint32_t OFF_BAR = OFF_INFO + 64;
     static constexpr uint32_t SMEM = OFF_BAR + 256;
 };
@@ -540,14 +540,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             const int n_tiles = tiles_of(qi);
             // keys of the part that this row may see (dense), from this half's first
             int lim = 0;
+            bool holes = false;
             if constexpr (DENSE) {
                 const PaItem& it = items[qi & 1];
                 lim = (int)min((int64_t)it.count, max((int64_t)0, it.pos0 + tok_off + 1 - it.lo)) - 32 * kh;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) holes = holes || pmax[(qi & 1) * 8 + 4 + w] != 0;
+                holes = __shfl_sync(0xffffffffu, holes, 0);
             }
             const uint32_t* vm = vmask + (qi & 1) * 64 + kh;
             float m_used = -INFINITY, l = 0.f;
             for (int u = 0; u < n_tiles; ++u, ++g) {
-                const uint32_t msk = DENSE ? low_bits(lim - u * PA_N) : vm[2 * u];  // keys that this row sees
+                uint32_t msk = DENSE ? low_bits(lim - u * PA_N) : vm[2 * u];  // keys that this row sees
+                if (DENSE && holes) {  // and that have a page (lane i looks for key i)
+                    const PaItem& it = items[qi & 1];
+                    const int key = u * PA_N + 32 * kh + lane;
+                    msk &= __ballot_sync(0xffffffffu, key < it.count && page_of(a.pv, it.b, it.lo + key).page >= 0);
+                }
                 if (!wait_warp(smem_u32(&bars->s_full), g & 1, abort, st, 0x2302)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t x[32];
@@ -738,9 +747,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                 for (int kb = 0; kb < 9; ++kb) prefetch_l2(qr + kb * 128);
             }
             if (!wait_warp(smem_u32(&bars->info_empty[slot]), (uint32_t)((qi >> 1) & 1) ^ 1u, abort, st, 0x2102)) return false;
-            int m = -1;
+            int m = -1, holes = 0;
             if constexpr (DENSE) {
                 m = it.count - 1;
+                // a part with positions that have no page: the softmax looks for them
+                // (nothing in its tiles otherwise)
+                if (it.count > 0) {
+                    uint32_t p0, p1, o;
+                    page_split(a.pv, (uint32_t)it.lo, p0, o);
+                    page_split(a.pv, (uint32_t)(it.lo + it.count - 1), p1, o);
+                    const int32_t* table = a.pv.table + it.b * a.pv.ld_table;
+#pragma unroll 4
+                    for (uint32_t p = p0 + quad * 32 + lane; p <= p1; p += 128)
+                        holes |= (int64_t)p >= a.pv.ld_table || (uint32_t)__ldg(table + p) >= (uint32_t)a.pv.num_pages;
+                    holes = __any_sync(0xffffffffu, holes);
+                }
             } else {
                 const int32_t* irow = a.idx + it.t0 * a.ld_idx + it.lo;
                 int32_t v[PA_SCAN_ROUNDS];
@@ -769,14 +790,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                     if (!it.ok && half == 0) report(st, DSA_ERR_INDEX, it.t0);
                 }
                 pmax[slot * 8 + quad] = m;
+                if (DENSE) pmax[slot * 8 + 4 + quad] = holes;
                 mbar_arrive(smem_u32(&bars->info_full[slot]));
             }
             __syncwarp();
             return true;
         };
-        // (groups are cut from the sequences: a token of none falls in no group)
-        if (DENSE && a.group > 1 && blockIdx.x == 0 && threadIdx.x == 32 * PA_EPI0)
-            report_no_sequence(a.sv, 0, a.total_q, st);
         uint32_t e = 0;     // items with tiles begun
         bool ok = nq == 0 || publish(0), pend = false;  // the (e - 1)-th item's epilogue is still to be done
         int64_t item_pend = 0;
@@ -816,6 +835,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
             if (qi + 1 < nq && !publish(qi + 1)) { ok = false; break; }
         }
         if (ok && pend) epilogue(it_pend, item_pend, e - 1);
+        // (groups are cut from the sequences: a token of none falls in no group)
+        if (DENSE && a.group > 1 && blockIdx.x == 0 && threadIdx.x == 32 * PA_EPI0)
+            report_no_sequence(a.sv, 0, a.total_q, st);
     }
     tc_fence_before();
     __syncthreads();

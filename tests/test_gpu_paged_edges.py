@@ -92,3 +92,26 @@ def test_scores_token_behind_the_last_sequence(fp8, lens):
     dsa.dsa_paged_scores(c.seqs, pages, u, s_row, 0, n + 2, got, ws)
     assert dsa.dsa_sync_status(ws)[0] == dsa.DSA_ERR_INDEX
     assert bool((got[n:] == NOT_SET).all())
+
+
+# ----------------------------------------------------------------------------- positions without a page
+@pytest.mark.parametrize("dtype,heads", [(BF, 128), (BF, 64), (BF, 5), (F32, 4)])
+@pytest.mark.parametrize("lens,page", [([(3, 100), (2, 60), (1, 16)], 16), ([(1, 3000), (2, 700)], 48),
+                                       ([(70, 260)], 1), ([(4, 4000)], 4096)])
+def test_attention_dense_positions_without_a_page(dtype, heads, lens, page):
+    """Skipped and recorded by the dense form of every type and head count, inside
+    a tile, across tiles and parts, and where no position of a row has a page."""
+    c = Cache(lens, page)
+    dk, dv = (576, 512) if dtype == BF else (64, 64)
+    kv = c.pool(dk, dtype)
+    per = [-(-k // page) for _, k in lens]
+    bad = [(b, p) for b, n in enumerate(per) for p in range(n) if p % 5 == 1 or n == 1]
+    for i, (b, p) in enumerate(bad):
+        c.table[b, p] = -1 if i % 2 else c.pages + i
+    valid = c.table.clone()
+    aa, q, out, lse, ws, pages, scale = _plan(c, kv, heads, dk, dv, dtype)
+    c.dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+    assert c.dsa.dsa_sync_status(ws)[0] == c.dsa.DSA_ERR_INDEX
+    valid[valid >= c.pages] = -1
+    c.table = valid
+    assert_attention(c, out, lse, attention(c, q, kv, kv[..., :dv], scale), dtype)
