@@ -489,9 +489,8 @@ DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const
  * leading columns), alignment as for dsa_sparse_attn (kv_page_stride a multiple
  * of 8 too), k_sel <= 2048; DSA_F32 with heads <= 32 and dk, dv in {32, 64, 96,
  * 128}, V its own pool or k's.  scale >= 0.
- * With fewer than 128 heads the bf16 dense form handles 128 / heads tokens of
- * a sequence together; a masked key among those tokens' own rows then has weight
- * 0 but must be finite.  Workspace: DSA_OP_PAGED_ATTN with k = k_sel. */
+ * A row depends on the keys that it attends to alone: later tokens' rows may hold
+ * anything.  Workspace: DSA_OP_PAGED_ATTN with k = k_sel. */
 DSA_API int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_args* aa, const int32_t* idx,
                            int64_t ld_idx, int32_t k_sel, void* ws, size_t ws_bytes, dsa_stream_t stream);
 

@@ -253,6 +253,25 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
         if (lane == 0) mbar_arrive(smem_u32(&bars->info_empty[qi & 1]));
     };
 
+    // Sets the values that are not finite to zero in the V rows row0 + i, i in `keys`, of
+    // the stage at sv (S of the tile is complete, its PV not issued).  Warps may do this
+    // together: they write the same zeros.
+    auto clear_not_finite = [&](uint32_t sv, int row0, uint32_t keys) {
+        for (; keys; keys &= keys - 1) {
+            const int row = row0 + __ffs((int)keys) - 1;
+            const uint32_t at = sv + (lane >> 3) * PA_BLK + pa_swz(row, lane & 7);  // 4 blocks x 8 chunks
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * i) : "memory");
+                uint32_t w = v;
+                if ((v & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                if ((v & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                if (w != v) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(w) : "memory");
+            }
+        }
+    };
+
     // Q of an item: three blocks into shared memory, six through registers and
     // this warp's staging tile (a row a lane) into tensor memory.  Rows past the
     // item are zero.  Loads take 4 rows x 128 bytes an instruction: a row a lane
@@ -566,6 +585,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
                 if (__any_sync(0xffffffffu, msk != 0xffffffffu)) {
+                    // A later token of the group may hold a NaN or an infinity, and 0 times
+                    // that is NaN.  V is the row's leading columns, so its score is then
+                    // not finite for any query: such masked keys' V values are set to
+                    // zero.  A row that sees the key has a NaN for its probability, or a
+                    // score of -inf and no weight on it.
+                    if constexpr (DENSE) {
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if ((x[i] & 0x7f800000u) == 0x7f800000u) odd |= 1u << i;
+                        odd = __reduce_or_sync(0xffffffffu, odd & ~msk);
+                        if (odd) {
+                            // (long complete: S was computed from it)
+                            if (!wait_warp(smem_u32(&bars->vfull[g % PA_NST]), (g / PA_NST) & 1, abort, st, 0x2305)) {
+                                ok = false;
+                                break;
+                            }
+                            clear_not_finite(s_v + g % PA_NST * PA_VST, 32 * kh, odd);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (!((msk >> i) & 1u)) x[i] = 0xff800000u;  // -inf

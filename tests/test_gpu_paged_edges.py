@@ -115,3 +115,36 @@ def test_attention_dense_positions_without_a_page(dtype, heads, lens, page):
     valid[valid >= c.pages] = -1
     c.table = valid
     assert_attention(c, out, lse, attention(c, q, kv, kv[..., :dv], scale), dtype)
+
+
+# ----------------------------------------------------------------------------- later tokens' rows
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("heads", [128, 64, 16, 5, 1])
+@pytest.mark.parametrize("lens,splits", [([(20, 150), (7, 64)], False), ([(130, 130)], False), ([(3, 5000)], True)])
+def test_attention_dense_later_rows_hold_anything(heads, bad, lens, splits):
+    """A NaN or an infinity in a token's cache row (a latent column of either half, a
+    rotated one, or all) reaches no earlier token, to the bit; with a NaN every
+    token from its own on is NaN."""
+    c = Cache(lens, 16)
+    kv = c.pool(576, BF)
+    aa, q, out, lse, ws, pages, scale = _plan(c, kv, heads, 576, 512, BF)
+    c.dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+    c.dsa.check_device_status(ws)
+    assert_attention(c, out, lse, attention(c, q, kv, kv[..., :512], scale), BF)
+    o0, l0 = out.clone(), lse.clone()
+    nq, n = lens[0]
+    pg, sl = c.rows(0)
+    for cols in (slice(3, 4), slice(300, 301), slice(570, 571), slice(0, 576)):
+        for t in {nq - 1, nq // 2, 1}:  # the token of position n - nq + t of sequence 0
+            at = n - nq + t
+            keep = kv[pg[at], sl[at]].clone()
+            kv[pg[at], sl[at], cols] = bad
+            out.fill_(NOT_SET), lse.fill_(NOT_SET)
+            c.dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+            kv[pg[at], sl[at]] = keep
+            clean = torch.ones(c.T, dtype=torch.bool, device="cuda")
+            clean[t:nq] = False
+            assert torch.equal(out[clean], o0[clean]) and torch.equal(lse[clean], l0[clean]), (cols, t)
+            if bad != bad:
+                assert bool(torch.isnan(out[t:nq]).all()) and bool(torch.isnan(lse[t:nq]).all())
+    c.dsa.check_device_status(ws)
