@@ -470,8 +470,9 @@ DSA_API int dsa_paged_scores(const dsa_seqs* seqs, const dsa_pages* pages, int32
 
 /* dsa_select over the paged indexer keys: ia->k_idx and ia->k_idx_scale are
  * the pools.  The scores pass through the workspace (DSA_OP_PAGED_SELECT), at
- * most 1 GiB of them at a time (or one row's, where that is more).  A position
- * without a valid page scores 0 here and is recorded. */
+ * most 1 GiB of them at a time (or one row's, where that is more); a workspace
+ * that was sized for a batch at least as large in every respect will do.  A
+ * position without a valid page scores 0 here and is recorded. */
 DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_indexer_args* ia, int32_t k,
                              int32_t* idx, int64_t ld_idx, void* ws, size_t ws_bytes, dsa_stream_t stream);
 
@@ -490,7 +491,12 @@ DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const
  * of 8 too), k_sel <= 2048; DSA_F32 with heads <= 32 and dk, dv in {32, 64, 96,
  * 128}, V its own pool or k's.  scale >= 0.
  * A row depends on the keys that it attends to alone: later tokens' rows may hold
- * anything.  Workspace: DSA_OP_PAGED_ATTN with k = k_sel. */
+ * anything.
+ * Workspace: DSA_OP_PAGED_ATTN with k = k_sel.  Few query rows are cut into parts
+ * of their keys, many are not, so the size of a smaller batch may be the larger one
+ * (at most 78 MB in bf16 on 148 SMs; (4 x 148 + total_q) x heads x (dv + 1) floats
+ * in fp32).  With less, from 256 bytes on, the call takes the parts that fit, which
+ * is slower; the sums' order, and so the last bits, follow the number of parts. */
 DSA_API int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_args* aa, const int32_t* idx,
                            int64_t ld_idx, int32_t k_sel, void* ws, size_t ws_bytes, dsa_stream_t stream);
 

@@ -513,7 +513,11 @@ struct PagedSelectLayout {
     int64_t rows;
 };
 
-PagedSelectLayout paged_select_layout(const dsa_seqs* s, const dsa_indexer_args* ia) {
+// ws_bytes: what there is (SIZE_MAX: as much as it takes).  Rows are cut to whole
+// blocks, so a shorter cache may ask for more than a longer one; a workspace of any
+// larger batch holds more than half of that, and the rows are handled in smaller
+// pieces then.
+PagedSelectLayout paged_select_layout(const dsa_seqs* s, const dsa_indexer_args* ia, size_t ws_bytes = SIZE_MAX) {
     PagedSelectLayout L;
     const WsLayout W = ws_layout(s, ia, 0, false, false);
     L.u = W.u;
@@ -524,12 +528,19 @@ PagedSelectLayout paged_select_layout(const dsa_seqs* s, const dsa_indexer_args*
     if (L.rows > 128) L.rows &= ~(int64_t)127;  // whole blocks of query rows
     if (L.rows < 1) L.rows = 1;
     if (L.rows > s->total_q) L.rows = s->total_q;
+    if (row && L.rows > 1 && ws_bytes > L.scores && (ws_bytes - L.scores) / row < (size_t)L.rows) {
+        int64_t fit = (int64_t)((ws_bytes - L.scores) / row);
+        if (fit > 128) fit &= ~(int64_t)127;
+        if (2 * fit >= L.rows) L.rows = fit;
+    }
     L.total = align256(L.scores + (size_t)L.rows * row);
     return L;
 }
 
-// Work items and parts of the paged attention.  Both follow from the shapes
-// alone, so the workspace size agrees with the call.
+// Work items and parts of the paged attention, from the shapes and from the
+// workspace that there is (SIZE_MAX: as much as it takes).  Fewer items are cut into
+// more parts, so a batch that has become smaller may ask for more than the larger one
+// did: it takes the parts that fit, or one each, which need the status header alone.
 struct PagedAttnPlan {
     int group;
     int64_t groups;
@@ -539,13 +550,17 @@ struct PagedAttnPlan {
 
 constexpr int kMaxParts = 64;
 
-PagedAttnPlan paged_attn_plan(const dsa_seqs* s, const dsa_attn_args* aa, int32_t k_sel) {
+PagedAttnPlan paged_attn_plan(const dsa_seqs* s, const dsa_attn_args* aa, int32_t k_sel, size_t ws_bytes = SIZE_MAX) {
     PagedAttnPlan p;
     p.group = 1;
     p.groups = s->total_q;
     p.splits = 1;
     const int64_t keys = k_sel > 0 ? k_sel : s->max_seqlen_k;
-    size_t rows, cols;
+    const size_t cols = aa->dtype == DSA_BF16 ? 512 : (size_t)aa->dv, item_rows = aa->dtype == DSA_BF16 ? 128 : (size_t)aa->heads;
+    auto rows = [&](int64_t n) { return (size_t)p.groups * (size_t)n * item_rows; };
+    auto bytes = [&](int64_t n) {  // of n parts an item: the header, log-sum-exps, partial rows
+        return n > 1 ? align256(align256(kHdr + rows(n) * 4) + rows(n) * cols * 4) : kHdr;
+    };
     if (aa->dtype == DSA_BF16) {
         if (k_sel == 0 && aa->heads <= 64) {
             p.group = 128 / aa->heads;
@@ -558,7 +573,7 @@ PagedAttnPlan paged_attn_plan(const dsa_seqs* s, const dsa_attn_args* aa, int32_
         const int64_t pairs = sm_count() / 2, tiles = (keys + 63) / 64;
         double best = 0;
         for (int64_t n = 1; n <= kMaxParts && n <= (tiles > 1 ? tiles : 1); ++n) {
-            if (n > 1 && p.groups * n > 4 * pairs) break;
+            if (n > 1 && (p.groups * n > 4 * pairs || bytes(n) > ws_bytes)) break;
             const int64_t waves = (p.groups * n + pairs - 1) / pairs;
             const double cost = (double)waves * (double)((tiles + n - 1) / n + 3 + (n > 1 ? 2 : 0)) +
                                 (n > 1 ? 1.5 + 0.03 * (double)(p.groups * n) : 0.0);
@@ -567,20 +582,17 @@ PagedAttnPlan paged_attn_plan(const dsa_seqs* s, const dsa_attn_args* aa, int32_
                 p.splits = (int)n;
             }
         }
-        rows = (size_t)p.groups * p.splits * 128;
-        cols = 512;
     } else {
         // four blocks an SM, parts of at least 64 keys
         const int64_t want = p.groups > 0 ? ((int64_t)sm_count() * 4 + p.groups - 1) / p.groups : 1;
         const int64_t most = (keys + 63) / 64;
         int64_t n = want < most ? want : most;
         p.splits = (int)(n < 1 ? 1 : n > kMaxParts ? kMaxParts : n);
-        rows = (size_t)p.groups * p.splits * aa->heads;
-        cols = (size_t)aa->dv;
+        while (p.splits > 1 && bytes(p.splits) > ws_bytes) --p.splits;
     }
     p.part_lse = kHdr;
-    p.part_o = p.splits > 1 ? align256(kHdr + rows * 4) : kHdr;
-    p.total = p.splits > 1 ? align256(p.part_o + rows * cols * 4) : kHdr;
+    p.part_o = p.splits > 1 ? align256(kHdr + rows(p.splits) * 4) : kHdr;
+    p.total = bytes(p.splits);
     return p;
 }
 
@@ -1166,7 +1178,7 @@ int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_ind
     if (!r) r = check_idx_pool(pages, ia->dtype, ia->k_idx, ia->k_idx_scale);
     if (r) return r;
     if (k < 1 || (seqs->total_q && (!idx || ld_idx < k)) || !aligned(idx, 4)) return DSA_ERR_INVALID_ARG;
-    const PagedSelectLayout L = paged_select_layout(seqs, ia);
+    const PagedSelectLayout L = paged_select_layout(seqs, ia, ws_bytes);
     r = check_ws(ws, ws_bytes, L.total);
     if (r) return r;
     if (seqs->total_q == 0) return DSA_OK;
@@ -1217,7 +1229,7 @@ int dsa_paged_attn(const dsa_seqs* seqs, const dsa_pages* pages, const dsa_attn_
     r = check_rows(seqs->total_q, aa->heads, aa->dk, aa->dtype, aa->q, aa->q_stride_tok, aa->q_stride_head);
     if (!r) r = check_rows(seqs->total_q, aa->heads, aa->dv, aa->dtype, aa->out, aa->out_stride_tok, aa->out_stride_head);
     if (r) return r;
-    const PagedAttnPlan P = paged_attn_plan(seqs, aa, k_sel);
+    const PagedAttnPlan P = paged_attn_plan(seqs, aa, k_sel, ws_bytes);
     r = check_ws(ws, ws_bytes, P.total);
     if (r) return r;
     if (seqs->total_q == 0) return DSA_OK;

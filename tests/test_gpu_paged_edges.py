@@ -148,3 +148,72 @@ def test_attention_dense_later_rows_hold_anything(heads, bad, lens, splits):
             if bad != bad:
                 assert bool(torch.isnan(out[t:nq]).all()) and bool(torch.isnan(lse[t:nq]).all())
     c.dsa.check_device_status(ws)
+
+
+# ----------------------------------------------------------------------------- a workspace kept while the batch shrinks
+@pytest.mark.parametrize("dtype,heads,selected", [(BF, 128, True), (BF, 128, False), (BF, 16, False), (F32, 4, False),
+                                                  (F32, 4, True)])
+def test_attention_workspace_of_a_larger_batch(dtype, heads, selected):
+    """Sized for 64 sequences, used for 20, 3 and 1: the call takes the parts that fit
+    (in bf16 the larger batch has none)."""
+    dk, dv = (576, 512) if dtype == BF else (64, 64)
+    k_sel = 2048 if selected else 0
+    ws = None
+    for n in (64, 20, 3, 1):
+        c = Cache([(1, 2500 + 7 * i) for i in range(n)], 64, seed=n)
+        sel = None
+        if selected:
+            sel = np.full((n, k_sel), -1, np.int32)
+            for t, p in enumerate(c.pos):
+                sel[t, :2000] = np.sort(c.rng.permutation(int(p) + 1)[:2000])
+            sel = torch.from_numpy(sel).cuda()
+        aa, q, out, lse, own, pages, scale = _plan(c, c.pool(dk, dtype), heads, dk, dv, dtype, k_sel=k_sel)
+        ws = own if ws is None else ws
+        want = attention(c, q, pages.kv, pages.kv[..., :dv], scale, sel)
+        for w in (ws, own):
+            out.fill_(NOT_SET), lse.fill_(NOT_SET)
+            c.dsa.dsa_paged_attn(c.seqs, pages, aa, sel, k_sel, w)
+            c.dsa.check_device_status(w)
+            assert_attention(c, out, lse, want, dtype)
+    with pytest.raises(c.dsa.DsaError):
+        c.dsa.dsa_paged_attn(c.seqs, pages, aa, sel, k_sel, own[:128])
+
+
+def test_select_workspace_of_a_longer_cache():
+    """Score rows are handled in whole blocks of queries, so a shorter cache may ask
+    for more than a longer one; a workspace of the longer one does, with the same
+    indices.  Several pieces of rows, with a k of each query's own."""
+    T, longer, shorter, page, k = 300, 1052700, 1048576, 4096, 64
+    c = Cache([(T, shorter)], page)
+    dsa = c.dsa
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+
+    def codes(*shape):
+        x = torch.randn(*shape, 128, generator=g, device="cuda")
+        return x.to(torch.float8_e4m3fn).view(torch.uint8)
+
+    pages = dsa.Pages(c.table, idx=codes(c.pages, page), idx_scale=torch.rand(c.pages, page, generator=g, device="cuda"))
+    k_rows = torch.randint(0, k + 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ia = dsa.paged_indexer_args(pages, codes(T), torch.ones(T, device="cuda"), torch.randn(128, 128, generator=g,
+                                                                                        device="cuda").to(BF), k_rows)
+    need = [dsa.dsa_workspace_size(dsa.DSA_OP_PAGED_SELECT, dsa.Seqs([0, T], [0, n]), k, ia) for n in (longer, shorter)]
+    assert need[0] < need[1]
+    got = []
+    for n in need:
+        ws = dsa.workspace(n)
+        idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+        dsa.dsa_paged_select(c.seqs, pages, ia, k, idx, ws)
+        dsa.check_device_status(ws)
+        got.append(idx)
+    assert torch.equal(got[0], got[1])
+    assert torch.equal((got[0] >= 0).sum(1).int(), k_rows.clamp(max=k))
+    # a row of the last piece, from its own call
+    one = dsa.Seqs([0, 1], [0, shorter])
+    ia1 = dsa.paged_indexer_args(pages, ia._keep[0][T - 1:], ia._keep[1][T - 1:], ia._keep[2], k_rows[T - 1:])
+    ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_PAGED_SELECT, one, k, ia1))
+    idx = torch.empty((1, k), dtype=torch.int32, device="cuda")
+    dsa.dsa_paged_select(one, pages, ia1, k, idx, ws)
+    assert torch.equal(idx[0], got[0][T - 1])
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_paged_select(c.seqs, pages, ia, k, got[0], dsa.workspace(need[1] // 3))
