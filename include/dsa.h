@@ -459,7 +459,7 @@ DSA_API int dsa_cache_append(const dsa_seqs* seqs, const dsa_pages* pages, const
 
 /* Indexer scores (as dsa_index_scores) of the folded queries u, s_row (from
  * dsa_fold) over the paged indexer keys k_idx / k_idx_scale (dtype DSA_E4M3, or
- * DSA_F32 with NULL scales), for query rows [row_begin, row_begin + row_count):
+ * DSA_F32 with NULL scales; s_row NULL there: ones), for query rows [row_begin, row_begin + row_count):
  * scores float [row_count, ld_scores], ReLU(s_row * s_k[s] * (u . k_s)) for
  * s <= pos, -inf for pos < s < ld_scores and for positions without a valid
  * page.  dsa_topk takes these scores.  Workspace: a status header. */

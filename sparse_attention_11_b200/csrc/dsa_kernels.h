@@ -292,7 +292,7 @@ struct PagedScoresArgs {
     PageView pv;
     int64_t max_seqlen_q, total_q;
     const void* u;         // folded queries [total_q, 128] (e4m3 codes or fp32)
-    const float* s_row;    // [total_q] (e4m3)
+    const float* s_row;    // [total_q] (fp32: nullable, ones)
     const void* k;         // key pool, rows of 128
     int64_t k_page_stride;
     const float* k_scale;  // key scales (e4m3)

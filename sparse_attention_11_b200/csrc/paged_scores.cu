@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(256) paged_scores_f32_kernel(const PagedScores
         const float4 v = __ldg((const float4*)((const float*)a.u + t * 128 + sub * 16) + i);
         q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
     }
+    const float sr = a.s_row ? __ldg(a.s_row + t) : 1.f;
     float* out = a.scores + (int64_t)blockIdx.y * a.ld;
     const int64_t s_end = min((int64_t)(blockIdx.x + 1) * PSF_KEYS, a.cols);
     for (int64_t s0 = (int64_t)blockIdx.x * PSF_KEYS; s0 < s_end; s0 += 32) {
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(256) paged_scores_f32_kernel(const PagedScores
         acc += __shfl_xor_sync(0xffffffffu, acc, 4);
         if (sub == 0 && s < s_end) {
             const bool seen = s <= ri.pos;
-            if (seen || a.fill) out[s] = seen && have ? ps_relu(acc) : a.fill ? -INFINITY : 0.f;
+            if (seen || a.fill) out[s] = seen && have ? ps_relu(__fmul_rn(acc, sr)) : a.fill ? -INFINITY : 0.f;
         }
     }
 }

@@ -217,3 +217,21 @@ def test_select_workspace_of_a_longer_cache():
     assert torch.equal(idx[0], got[0][T - 1])
     with pytest.raises(dsa.DsaError):
         dsa.dsa_paged_select(c.seqs, pages, ia, k, got[0], dsa.workspace(need[1] // 3))
+
+
+# ----------------------------------------------------------------------------- the queries' scales
+def test_scores_f32_scale_of_the_query():
+    """s_row multiplies the fp32 scores too: one rounding more than without it."""
+    c = Cache([(3, 200), (1, 65)], 16)
+    dsa = c.dsa
+    k, _ = c.key_pool(False)
+    u, s_row = c.randn(c.T, 128), 0.5 + torch.rand(c.T, device="cuda")
+    pages = dsa.Pages(c.table, idx=k)
+    ws = dsa.workspace(256)
+    plain, ones, got = (torch.empty((c.T, 200), device="cuda") for _ in range(3))
+    dsa.dsa_paged_scores(c.seqs, pages, u, None, 0, c.T, plain, ws)
+    dsa.dsa_paged_scores(c.seqs, pages, u, torch.ones(c.T, device="cuda"), 0, c.T, ones, ws)
+    dsa.dsa_paged_scores(c.seqs, pages, u, s_row, 0, c.T, got, ws)
+    dsa.check_device_status(ws)
+    assert torch.equal(plain, ones)
+    assert torch.equal(got, plain * s_row[:, None])
