@@ -478,8 +478,8 @@ def dsa_cache_append(seqs, pages, ap, ws):
 
 def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
     """Indexer scores of folded queries (u, s_row from dsa_fold) over the paged
-    indexer keys; scores float32 [row_count, >= max_seqlen_k], -inf past a row's
-    position.  dsa_topk selects from them."""
+    indexer keys; scores float32 [row_count, >= max_seqlen_k], rows one after the
+    other, -inf past a row's position.  dsa_topk selects from them."""
     _here(u, scores, pages.table, ws)
     _need(s_row is None or (s_row.device == u.device and s_row.dtype == torch.float32 and s_row.is_contiguous()
                             and s_row.numel() >= seqs.c.total_q), "s_row: contiguous float32 [T]")
@@ -490,10 +490,12 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
           "u: contiguous [T, 128] of the pool's type")
     _need(scores.dtype == torch.float32 and (st[1] == 1 or cols == 1) and rows >= row_count and cols >= c.max_seqlen_k,
           "scores: float32 [row_count, >= max_seqlen_k]")
+    # (the -inf behind a row fills it up to the next row: columns beside a view are not this call's)
+    _need(row_count <= 1 or st[0] == cols, "scores: rows one after the other")
     fp8 = dt == torch.uint8
     _check(_lib.dsa_paged_scores(ctypes.byref(c), ctypes.byref(pages.c), DSA_E4M3 if fp8 else DSA_F32, u.data_ptr(),
                                  _ptr(s_row), pages.idx.data_ptr(), _ptr(pages.idx_scale) if fp8 else None, row_begin,
-                                 row_count, scores.data_ptr(), cols if rows == 1 else st[0], ws.data_ptr(), ws.numel(),
+                                 row_count, scores.data_ptr(), cols, ws.data_ptr(), ws.numel(),
                                  _stream()), "dsa_paged_scores")
 
 

@@ -235,3 +235,24 @@ def test_scores_f32_scale_of_the_query():
     dsa.check_device_status(ws)
     assert torch.equal(plain, ones)
     assert torch.equal(got, plain * s_row[:, None])
+
+
+# ----------------------------------------------------------------------------- what the binding refuses
+def test_scores_columns_beside_a_view():
+    """The -inf of a row ends with the row: a view of a wider tensor keeps what lies
+    beside it, so several of its rows are refused and one is served."""
+    c = Cache([(3, 200), (1, 65)], 16)
+    dsa = c.dsa
+    k, _ = c.key_pool(False)
+    pages, u, ws = dsa.Pages(c.table, idx=k), c.randn(c.T, 128), dsa.workspace(256)
+    buf = torch.full((c.T, 350), NOT_SET, device="cuda")
+    want = torch.empty((c.T, 220), device="cuda")
+    dsa.dsa_paged_scores(c.seqs, pages, u, None, 0, c.T, want, ws)
+    for view in (buf[:, :220], buf[:2, :220]):
+        with pytest.raises(ValueError):
+            dsa.dsa_paged_scores(c.seqs, pages, u, None, 0, len(view), view, ws)
+    for t in range(c.T):
+        dsa.dsa_paged_scores(c.seqs, pages, u, None, t, 1, buf[t:, 100:320], ws)
+    dsa.check_device_status(ws)
+    assert torch.equal(buf[:, 100:320], want)
+    assert bool((buf[:, :100] == NOT_SET).all()) and bool((buf[:, 320:] == NOT_SET).all())
