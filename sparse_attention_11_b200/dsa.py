@@ -153,6 +153,7 @@ class Seqs:
         self.cu_k = ck.to(device)
         self.c = dsa_seqs(len(cq) - 1, int(cq[-1]), int(ck[-1]), int(lq.max()) if len(lq) else 0,
                           int(lk.max()) if len(lk) else 0, self.cu_q.data_ptr(), self.cu_k.data_ptr())
+        self._index = self.cu_q.get_device()
 
     @property
     def total_q(self):
@@ -297,17 +298,17 @@ def _dtype(t):
     return _DTYPES[t.dtype]
 
 
-def _here(*tensors):
-    """Refuse tensors of another device than the current one, whose stream the
-    call would use."""
+def _here(seqs, *tensors):
+    """Refuse tensors, and a batch's lengths, of another device than the current
+    one, whose stream the call would use."""
     dev = tensors[0].get_device()  # (-1: not a CUDA tensor)
-    if dev >= 0 and dev == _device():
+    if dev >= 0 and dev == _device() and seqs._index == dev:
         for t in tensors:
             if t.get_device() != dev:
                 break
         else:
             return dev
-    raise ValueError("tensors must be on the current CUDA device")
+    raise ValueError("tensors and lengths must be on the current CUDA device")
 
 
 def rope_table(positions, dim, base=10000.0, device="cuda"):
@@ -437,7 +438,7 @@ def _rows_of(seqs, t, shape, dtype):
 def dsa_norm_rope(seqs, ra, x, y, ws):
     """y[t,h,:] = the transform ra (row_args or None) of x[t,h,:] at token t's
     position; x, y [T,H,dim] bfloat16 or float32 (y may be x)."""
-    dev = _here(x, y, ws)
+    dev = _here(seqs, x, y, ws)
     _need(ra is None or ra._index is None or ra._index == dev, "weight and cos_sin are on x's device")
     sh, dt = x.shape, x.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt)
@@ -451,7 +452,7 @@ def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
     """Backward of dsa_norm_rope: d_x [T,H,dim] (x's type) and d_weight (float32
     [norm_dim] or None) are written from x (None without a norm) and d_y.  ws of
     dsa_workspace_size(DSA_OP_NORM_ROPE_BWD, seqs, norm_dim) bytes."""
-    dev = _here(*[t for t in (x, d_y, d_x, d_weight, ws) if t is not None])
+    dev = _here(seqs, *[t for t in (x, d_y, d_x, d_weight, ws) if t is not None])
     _need(ra is None or ra._index is None or ra._index == dev, "weight and cos_sin are on x's device")
     sh, dt = d_y.shape, d_y.dtype
     xp, xt, xh = _rows_of(seqs, x, sh, dt) if x is not None else (None, sh[1] * sh[2], sh[2])
@@ -468,7 +469,7 @@ def dsa_norm_rope_bwd(seqs, ra, x, d_y, d_x, d_weight, ws):
 def dsa_cache_append(seqs, pages, ap, ws):
     """Append the queries' tokens (append_args) to the paged cache at their
     positions.  seqs holds the lengths after the append."""
-    _here(pages.table, ws)
+    _here(seqs, pages.table, ws)
     c = seqs.c
     pages.need(c)
     _need(ap._rows >= c.total_q and ap._keep[0] is pages, "a row per query token, appended to these pages")
@@ -480,7 +481,7 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
     """Indexer scores of folded queries (u, s_row from dsa_fold) over the paged
     indexer keys; scores float32 [row_count, >= max_seqlen_k], rows one after the
     other, -inf past a row's position.  dsa_topk selects from them."""
-    _here(u, scores, pages.table, ws)
+    _here(seqs, u, scores, pages.table, ws)
     _need(s_row is None or (s_row.device == u.device and s_row.dtype == torch.float32 and s_row.is_contiguous()
                             and s_row.numel() >= seqs.c.total_q), "s_row: contiguous float32 [T]")
     c, dt, us, (rows, cols), st = seqs.c, u.dtype, u.shape, scores.shape, scores.stride()
@@ -511,7 +512,7 @@ def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
 def dsa_paged_select(seqs, pages, ia, k, idx, ws):
     """dsa_select over the paged indexer keys (ia from paged_indexer_args).  ws
     of dsa_workspace_size(DSA_OP_PAGED_SELECT, seqs, k, ia) bytes."""
-    _here(idx, pages.table, ws)
+    _here(seqs, idx, pages.table, ws)
     pages.need(seqs.c)
     _need(pages.idx is not None and (ia.k_idx or 0) == pages.idx.data_ptr()
           and (not ia.k_idx_scale or (pages.idx_scale is not None and ia.k_idx_scale == pages.idx_scale.data_ptr())),
@@ -529,14 +530,14 @@ def dsa_paged_attn(seqs, pages, aa, idx, k_sel, ws):
     paged_attn_args): dense causal with idx None and k_sel 0, else over idx
     int32 [T, >= k_sel] of local positions (-1 unused).  ws of
     dsa_workspace_size(DSA_OP_PAGED_ATTN, seqs, k_sel, None, aa) bytes."""
-    _here(pages.table, ws)
+    _here(seqs, pages.table, ws)
     c = seqs.c
     pages.need(c)
     _need(aa._rows >= c.total_q and aa._keep[0] is pages, "a q row per token, arguments over these pages")
     ip, ld = None, 0
     if idx is not None:
         (rows, cols), st = idx.shape, idx.stride()
-        _here(idx)
+        _here(seqs, idx)
         _need(idx.dtype == torch.int32 and rows >= c.total_q and (st[1] == 1 or cols == 1) and cols >= k_sel,
               "idx: int32 [T, >= k_sel]")
         ip, ld = idx.data_ptr(), st[0] if rows > 1 else max(cols, k_sel)

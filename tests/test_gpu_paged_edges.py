@@ -256,3 +256,33 @@ def test_scores_columns_beside_a_view():
     dsa.check_device_status(ws)
     assert torch.equal(buf[:, 100:320], want)
     assert bool((buf[:, :100] == NOT_SET).all()) and bool((buf[:, 320:] == NOT_SET).all())
+
+
+def test_lengths_on_another_device_are_refused():
+    c = Cache([(2, 50), (1, 3)], 16)
+    dsa = c.dsa
+    idx, sc = c.key_pool()
+    kv, new = c.pool(576, BF), c.randn(3, 576, dtype=BF)
+    pages = dsa.Pages(c.table, kv=kv, idx=idx, idx_scale=sc)
+    q, out = c.randn(3, 128, 576, dtype=BF), torch.empty(3, 128, 512, dtype=BF, device="cuda")
+    u, s_row = torch.zeros(3, 128, dtype=torch.uint8, device="cuda"), torch.ones(3, device="cuda")
+    sel = torch.zeros(3, 8, dtype=torch.int32, device="cuda")
+    ia = dsa.paged_indexer_args(pages, u, s_row, torch.ones(128, 128, dtype=BF, device="cuda"))
+    aa, ap = dsa.paged_attn_args(pages, q, 0.1, out), dsa.append_args(pages, kv_new=new)
+    ws = dsa.workspace(1 << 26)
+
+    def calls(s):
+        return [lambda: dsa.dsa_norm_rope(s, None, q, q, ws),
+                lambda: dsa.dsa_norm_rope_bwd(s, None, None, q, torch.empty_like(q), None, ws),
+                lambda: dsa.dsa_cache_append(s, pages, ap, ws),
+                lambda: dsa.dsa_paged_scores(s, pages, u, s_row, 0, 3, torch.empty(3, 50, device="cuda"), ws),
+                lambda: dsa.dsa_paged_select(s, pages, ia, 8, sel, ws),
+                lambda: dsa.dsa_paged_attn(s, pages, aa, None, 0, ws),
+                lambda: dsa.dsa_paged_attn(s, pages, aa, sel, 8, ws)]
+
+    for f in calls(dsa.Seqs([0, 2, 3], [0, 50, 53], device="cpu")):
+        with pytest.raises(ValueError):
+            f()
+    for f in calls(c.seqs):
+        f()
+    dsa.check_device_status(ws)
