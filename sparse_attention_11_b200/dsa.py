@@ -501,8 +501,18 @@ def dsa_paged_scores(seqs, pages, u, s_row, row_begin, row_count, scores, ws):
 
 
 def paged_indexer_args(pages, q_idx, q_idx_scale, w_index, k_per_row=None):
-    """indexer_args over the indexer-key pool of `pages`."""
+    """indexer_args over the indexer-key pool of `pages`: q_idx [T, 128] of the
+    pool's type, with q_idx_scale float32 [T] and a bfloat16 w_index [128, 128] for
+    codes, None and a float32 one for float32; k_per_row int32 [T] or None."""
     _need(pages.idx is not None and pages.idx.dtype == q_idx.dtype, "q_idx has the indexer-key pool's type")
+    _need(q_idx.dim() == 2 and q_idx.shape[1] == 128 and q_idx.is_contiguous(), "q_idx: contiguous [T, 128]")
+    fp8, rows = q_idx.dtype == torch.uint8, q_idx.shape[0]
+    _need(w_index.dtype == (torch.bfloat16 if fp8 else torch.float32) and w_index.shape == (128, 128)
+          and w_index.is_contiguous(), "w_index: contiguous [128, 128], bfloat16 for codes, else float32")
+    _need((q_idx_scale is not None) == fp8, "q_idx_scale: for codes")
+    for t, dt in (q_idx_scale, torch.float32), (k_per_row, torch.int32):
+        _need(t is None or (t.dtype == dt and t.is_contiguous() and t.numel() >= rows),
+              "q_idx_scale: contiguous float32 [T], k_per_row: contiguous int32 [T]")
     _need(all(t is None or t.device == pages.idx.device for t in (q_idx, q_idx_scale, w_index, k_per_row)),
           "queries, weights and k_per_row are on the pools' device")
     return indexer_args(q_idx, q_idx_scale, w_index, pages.idx, pages.idx_scale if q_idx.dtype == torch.uint8 else None,
