@@ -362,7 +362,8 @@ DSA_API int dsa_forward_host(const dsa_seqs* seqs, const dsa_indexer_args* ia, c
  * rounding at the end.  Aligned rows (16-byte aligned pointers and strides,
  * dim, norm_dim, rope_begin and rope_dim multiples of 8, half-split rope_dim of
  * 16) are moved in 16-byte pieces; any other rows take a scalar path with the
- * same results up to the order of sums.  dim <= 2048.                        */
+ * same results up to the roundings of their sums and products.  The reciprocal
+ * root is within 2 ulp.  dim <= 2048.                                        */
 typedef struct dsa_row_args {
     int32_t norm_dim;
     float eps;

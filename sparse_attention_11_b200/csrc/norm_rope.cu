@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ss = fmaf(xv[i][e], xv[i][e], ss);
             ss = group_sum<G>(ss);
-            const float rstd = live ? rsqrtf(fmaf(ss, inv_n, a.ra.eps)) : 0.f;  // no row: zeros throughout
+            const float rstd = live ? row_rstd(fmaf(ss, inv_n, a.ra.eps)) : 0.f;  // no row: zeros throughout
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (gl + G * i) * 8;
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const 
     const int lane = (int)lane_id(), warp = (int)warp_id(), n = a.ra.norm_dim;
     const RowXform& ra = a.ra;
     const int h = ra.rope_dim >> 1;
+    const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
     next_grid();
     float* acc = nr_sm + warp * n;
     for (int c = lane; c < n; c += 32) acc[c] = 0.f;
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_bwd_scalar_kernel(const 
             }
             ss = group_sum<32>(ss);
             dot = group_sum<32>(dot);
-            rstd = 1.0f / sqrtf(ss / (float)n + ra.eps);
-            k = dot * rstd / (float)n;
+            rstd = row_rstd(fmaf(ss, inv_n, ra.eps));
+            k = dot * rstd * inv_n;
         }
         for (int c = lane; c < a.dim; c += 32) {
             const float g = grad(c);

@@ -104,6 +104,12 @@ DSA_DEV float group_sum(float x) {
     return x;
 }
 
+// A row's reciprocal root mean square, from mean square + eps.  rsqrtf is within 2
+// ulp; 1 / sqrtf measured 43.6 us against 41.6 (backward of 232K heads of 128 in
+// bf16) and 33.8 against 33.1 (forward).  Every path takes this one, so that a row's
+// alignment does not change it.
+DSA_DEV float row_rstd(float ms) { return rsqrtf(ms); }
+
 // Rotate the chunks of this row that lie in the rotated columns, in place;
 // sgn = 1 rotates by the position's angles, -1 back (the transpose).
 // Interleaved pairs lie inside an 8-column chunk.  Half-split pairs are
@@ -250,7 +256,7 @@ DSA_DEV void row_forward(const Raw8<T> (&r)[NC], T* y, const RowXform& ra, int d
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
         ss = group_sum<G>(ss);
-        const float rstd = rsqrtf(ss / (float)ra.norm_dim + ra.eps);  // within 2 ulp
+        const float rstd = row_rstd(ss / (float)ra.norm_dim + ra.eps);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (gl + G * i) * 8;
@@ -282,7 +288,7 @@ DSA_DEV void row_forward_scalar(const T* x, T* y, const RowXform& ra, int dim, c
             const float a = load1(x + c);
             ss = fmaf(a, a, ss);
         }
-        rstd = 1.0f / sqrtf(group_sum<32>(ss) / (float)ra.norm_dim + ra.eps);
+        rstd = row_rstd(group_sum<32>(ss) / (float)ra.norm_dim + ra.eps);
     }
     __syncwarp();
     auto value = [&](int c) {
