@@ -45,3 +45,33 @@ def test_norm_is_the_same_off_alignment(dim):
         a, b = _both(dim, n, f)
         assert torch.equal(a, b), f.__name__
     dsa.check_device_status(ws)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,heads", [(128, 32), (256, 4), (576, 1), (75, 3)])
+def test_backward_captured(dim, heads, dtype):
+    """The kernel that sums the weight's gradient starts before its terms are written:
+    captured several times in a row, replayed with new inputs, the bits of the call."""
+    from sparse_attention_11_b200 import dsa
+
+    T = 700
+    seqs = dsa.Seqs([0, T], [0, T])
+    ra = dsa.row_args(norm_dim=dim, weight=torch.randn(dim, device="cuda"), rope_dim=24, rope_begin=8,
+                      cos_sin=dsa.rope_table(T, 24))
+    x, dy = (torch.empty(T, heads, dim, dtype=dtype, device="cuda") for _ in range(2))
+    dx, dw = torch.empty_like(x), [torch.empty(dim, device="cuda") for _ in range(3)]
+    ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_NORM_ROPE_BWD, seqs, dim))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        for w in dw:
+            dsa.dsa_norm_rope_bwd(seqs, ra, x, dy, dx, w, ws)
+    for i in range(5):
+        x.copy_(torch.randn(x.shape, device="cuda")), dy.copy_(torch.randn(x.shape, device="cuda"))
+        g.replay()
+        got = [t.clone() for t in (dx, *dw)]
+        want = torch.empty_like(dw[0])
+        dsa.dsa_norm_rope_bwd(seqs, ra, x, dy, dx, want, ws)
+        assert torch.equal(got[0], dx) and all(torch.equal(t, want) for t in got[1:])
+    dsa.check_device_status(ws)

@@ -286,3 +286,64 @@ def test_lengths_on_another_device_are_refused():
     for f in calls(c.seqs):
         f()
     dsa.check_device_status(ws)
+
+
+# ----------------------------------------------------------------------------- parts and their join
+@pytest.mark.parametrize("heads", [128, 16])
+@pytest.mark.parametrize("n", [20000, 65536])
+def test_attention_bf16_many_parts(heads, n):
+    """One token over a long cache: more parts than lanes, up to the most there are."""
+    c = Cache([(1, n)], 64)
+    kv = torch.randn(c.pages, 64, 576, device="cuda").to(BF)
+    aa, q, out, lse, ws, pages, scale = _plan(c, kv, heads, 576, 512, BF)
+    assert ws.numel() > 256 + 32 * 128 * 513 * 4  # more than 32
+    c.dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+    c.dsa.check_device_status(ws)
+    assert_attention(c, out, lse, attention(c, q, kv, kv[..., :512], scale), BF)
+
+
+@pytest.mark.parametrize("dtype,heads", [(BF, 128), (BF, 16), (F32, 4)])
+@pytest.mark.parametrize("selected", [False, True])
+def test_attention_parts_captured(dtype, heads, selected):
+    """The kernel that joins parts starts before the parts are done: captured and
+    replayed, with lengths that grow and shrink (parts at the end become empty), beside
+    a second graph with a workspace of its own."""
+    dk, dv = (576, 512) if dtype == BF else (64, 64)
+    bound, k_sel = 9000, 1500 if selected else 0
+    sides = []
+    for seed in (1, 2):
+        c = Cache([(1, bound), (2, bound)], 64, seed=seed)
+        sel = torch.full((c.T, k_sel), -1, dtype=torch.int32, device="cuda") if selected else None
+        plan = _plan(c, c.pool(dk, dtype), heads, dk, dv, dtype, k_sel=k_sel)
+        assert plan[4].numel() > 256
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        aa, q, out, lse, ws, pages, scale = plan
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):
+                c.dsa.dsa_paged_attn(c.seqs, pages, aa, sel, k_sel, ws)
+        sides.append((c, sel, plan, st, g))
+    for lens in ((9000, 9000), (1, 2), (5000, 64), (130, 8999)):
+        for c, sel, (aa, q, out, lse, ws, pages, scale), st, g in sides:
+            q.copy_(c.randn(c.T, heads, dk, dtype=dtype))
+            out.fill_(NOT_SET), lse.fill_(NOT_SET)
+            c.seqs.cu_k.copy_(torch.tensor([0, lens[0], lens[0] + lens[1]]))
+            live = Cache([(1, lens[0]), (2, lens[1])], 64)
+            live.table = c.table
+            if selected:
+                s = np.full((c.T, k_sel), -1, np.int32)
+                for t, p in enumerate(live.pos):
+                    n = min(int(p) + 1, k_sel)
+                    s[t, :n] = np.sort(c.rng.permutation(int(p) + 1)[:n])
+                sel.copy_(torch.from_numpy(s))
+        torch.cuda.synchronize()
+        for *_, st, g in sides:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for c, sel, (aa, q, out, lse, ws, pages, scale), st, g in sides:
+            c.dsa.check_device_status(ws)
+            live = Cache([(1, lens[0]), (2, lens[1])], 64)
+            live.table = c.table
+            assert_attention(live, out, lse, attention(live, q, pages.kv, pages.kv[..., :dv], scale, sel), dtype)
