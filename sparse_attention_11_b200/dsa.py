@@ -341,6 +341,11 @@ def row_args(norm_dim=0, weight=None, eps=1e-6, rope_begin=0, rope_dim=0, cos_si
     return a
 
 
+def _pool_row(p):
+    """Elements between the rows of a page (any, in pages of one row)."""
+    return p.stride(1) if p.shape[1] > 1 else p.shape[2]
+
+
 class Pages:
     """A page table and its pools: table int32 [batch, pages per sequence];
     kv [num_pages, page_size, >=dk], v (its own pool, or None), idx [num_pages,
@@ -368,8 +373,10 @@ class Pages:
         self.table, self.kv, self.v, self.idx, self.idx_scale = table, kv, v, idx, idx_scale
         self.batch, self.positions = table.shape[0], table.shape[1] * size
 
-        def page(p):
-            return 0 if p is None else p.stride(0)
+        def page(p):  # (any, in a pool of one page)
+            if p is None or n > 1:
+                return 0 if p is None else p.stride(0)
+            return size * (_pool_row(p) if p.dim() == 3 else 1)
 
         self.c = dsa_pages(size, n, table.data_ptr(), max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else
                            table.stride(0), page(kv), page(v), page(idx), page(idx_scale))
@@ -393,14 +400,16 @@ def append_args(pages, kv_new=None, kv_row=None, idx_new=None, idx_row=None):
     if kv_new is not None:
         _need(pages.kv is not None and kv_new.dtype == pages.kv.dtype, "kv_new has the KV pool's type")
         _need(kv_new.dim() == 2 and kv_new.stride(1) == 1 and kv_new.shape[1] <= pages.kv.shape[2], "kv_new: [T, dim]")
-        a.dim, a.kv_new, a.kv_new_stride = kv_new.shape[1], kv_new.data_ptr(), kv_new.stride(0)
-        a.kv, a.kv_stride = pages.kv.data_ptr(), pages.kv.stride(1)
+        a.dim, a.kv_new = kv_new.shape[1], kv_new.data_ptr()
+        a.kv_new_stride = kv_new.stride(0) if kv_new.shape[0] > 1 else a.dim
+        a.kv, a.kv_stride = pages.kv.data_ptr(), _pool_row(pages.kv)
         a.kv_row = ctypes.pointer(kv_row) if kv_row is not None else None
     if idx_new is not None:
         _need(pages.idx is not None and _dtype(idx_new) == a.dtype, "idx_new has kv_new's type")
         _need(idx_new.dim() == 2 and idx_new.stride(1) == 1 and idx_new.shape[1] == 128, "idx_new: [T, 128]")
         a.idx_dtype = DSA_E4M3 if pages.idx.dtype == torch.uint8 else DSA_F32
-        a.idx_new, a.idx_new_stride, a.idx = idx_new.data_ptr(), idx_new.stride(0), pages.idx.data_ptr()
+        a.idx_new, a.idx = idx_new.data_ptr(), pages.idx.data_ptr()
+        a.idx_new_stride = idx_new.stride(0) if idx_new.shape[0] > 1 else 128
         a.idx_scale = pages.idx_scale.data_ptr() if pages.idx_scale is not None else None
         a.idx_row = ctypes.pointer(idx_row) if idx_row is not None else None
     a._keep = (pages, kv_new, kv_row, idx_new, idx_row)
@@ -418,21 +427,27 @@ def paged_attn_args(pages, q, scale, out, lse=None):
     _need(all(t is None or t.device == kv.device for t in (q, out, lse)), "q, out and lse are on the pools' device")
     _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:2]),
           "lse: contiguous float32 [T,H]")
-    a = dsa_attn_args(_dtype(q), q.shape[1], q.shape[2], out.shape[2], q.data_ptr(), q.stride(0), q.stride(1),
-                      kv.data_ptr(), kv.stride(1), v.data_ptr(), v.stride(1), float(scale), out.data_ptr(), out.stride(0),
-                      out.stride(1), lse.data_ptr() if lse is not None else None)
+    a = dsa_attn_args(_dtype(q), q.shape[1], q.shape[2], out.shape[2], q.data_ptr(), *_row_strides(q.shape, q.stride()),
+                      kv.data_ptr(), _pool_row(kv), v.data_ptr(), _pool_row(v), float(scale), out.data_ptr(),
+                      *_row_strides(out.shape, out.stride()), lse.data_ptr() if lse is not None else None)
     a._keep = (pages, q, out, lse)
     a._rows = q.shape[0]
     return a
+
+
+def _row_strides(shape, s):
+    """Token and head strides of rows [T, heads, dim]; a dimension of one, whose
+    stride torch leaves open, gets that of rows one after the other."""
+    head = s[1] if shape[1] > 1 else shape[2]
+    return s[0] if shape[0] > 1 else shape[1] * max(head, shape[2]), head
 
 
 def _rows_of(seqs, t, shape, dtype):
     s = t.stride()
     if t.shape != shape or len(s) != 3 or shape[0] < seqs.c.total_q or (s[2] != 1 and shape[2] > 1) or t.dtype != dtype:
         raise ValueError("rows: [T, heads, dim] of one shape and type, contiguous columns")
-    # (a dimension of one has any stride)
-    return t.data_ptr(), s[0] if shape[0] > 1 else max(s[0], shape[1] * max(s[1], shape[2])), \
-        s[1] if shape[1] > 1 else max(s[1], shape[2])
+    head = s[1] if shape[1] > 1 else shape[2]  # (as _row_strides, without a call)
+    return t.data_ptr(), s[0] if shape[0] > 1 else shape[1] * max(head, shape[2]), head
 
 
 def dsa_norm_rope(seqs, ra, x, y, ws):

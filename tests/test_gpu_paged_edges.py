@@ -347,3 +347,47 @@ def test_attention_parts_captured(dtype, heads, selected):
             live = Cache([(1, lens[0]), (2, lens[1])], 64)
             live.table = c.table
             assert_attention(live, out, lse, attention(live, q, pages.kv, pages.kv[..., :dv], scale, sel), dtype)
+
+
+# ----------------------------------------------------------------------------- strides of dimensions of one
+def _loose(t, dims):
+    """The same tensor with other strides in its dimensions of one."""
+    st = list(t.stride())
+    for d in dims:
+        assert t.shape[d] == 1
+        st[d] = 3
+    return t.as_strided(t.shape, st)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_strides_of_dimensions_of_one(dtype):
+    """One token, one head, pages of one row, a pool of one page: their strides mean
+    nothing and refuse nothing, and keep no call from the aligned path."""
+    dk, dv = (576, 512) if dtype == BF else (64, 64)
+    for heads, page, n in ((1, 1, 9), (4, 1, 9), (4, 16, 9), (1, 16, 9)):
+        c = Cache([(1, n)], page, spare=0)
+        dsa = c.dsa
+        kv = c.pool(dk, dtype)
+        q, new = c.randn(1, heads, dk, dtype=dtype), c.randn(1, dk, dtype=dtype)
+        out = torch.full((1, heads, dv), NOT_SET, dtype=dtype, device="cuda")
+        one = [d for d in (0, 1) if q.shape[d] == 1]
+        pools = [d for d in (0, 1) if kv.shape[d] == 1]
+        pages = dsa.Pages(c.table, kv=_loose(kv, pools))
+        ws = dsa.workspace(1 << 20)
+        dsa.dsa_cache_append(c.seqs, pages, dsa.append_args(pages, kv_new=_loose(new, [0])), ws)
+        pg, sl = c.rows(0)
+        assert torch.equal(kv[pg[-1], sl[-1]], new[0])
+        y = torch.empty_like(q)
+        dsa.dsa_norm_rope(c.seqs, dsa.row_args(norm_dim=dk), _loose(q, one), _loose(y, one), ws)
+        want = torch.empty_like(q)
+        dsa.dsa_norm_rope(c.seqs, dsa.row_args(norm_dim=dk), q, want, ws)
+        assert torch.equal(y, want)
+        aa = dsa.paged_attn_args(pages, _loose(q, one), 0.1, _loose(out, one), lse := torch.empty(1, heads, device="cuda"))
+        dsa.dsa_paged_attn(c.seqs, pages, aa, None, 0, ws)
+        dsa.check_device_status(ws)
+        assert_attention(c, out, lse, attention(c, q, kv, kv[..., :dv], 0.1), dtype)
+    idx, sc = c.key_pool()
+    pages = dsa.Pages(c.table, idx=_loose(idx, [0]), idx_scale=_loose(sc, [0]))
+    key = c.randn(1, 128, dtype=dtype)
+    dsa.dsa_cache_append(c.seqs, pages, dsa.append_args(pages, idx_new=_loose(key, [0])), ws)
+    dsa.check_device_status(ws)
