@@ -492,7 +492,9 @@ DSA_API int dsa_paged_select(const dsa_seqs* seqs, const dsa_pages* pages, const
  * of 8 too), k_sel <= 2048; DSA_F32 with heads <= 32 and dk, dv in {32, 64, 96,
  * 128}, V its own pool or k's.  scale >= 0.
  * A row depends on the keys that it attends to alone: later tokens' rows may hold
- * anything.
+ * anything.  In bf16 the probabilities, relative to the running maximum, are rounded
+ * to bf16 for P V (half a step, 2^-8 of each at most, beside the output's own rounding);
+ * their sum, the maximum and O are fp32.
  * Workspace: DSA_OP_PAGED_ATTN with k = k_sel.  Few query rows are cut into parts
  * of their keys, many are not, so the size of a smaller batch may be the larger one
  * (at most 78 MB in bf16 on 148 SMs; (4 x 148 + total_q) x heads x (dv + 1) floats

@@ -10,8 +10,11 @@
 // twice, 1344 tensor cycles a tile; halving the contraction between the CTAs of a
 // cluster (as attn_tc.cu does) costs an exchange of partial scores and
 // probabilities through distributed shared memory, and measured 2590 us here
-// (two chunks of 300-700 tokens over 3000-5000 keys, 128 heads) against 1700-1850
-// us: 0.45 of the burst matrix rate, 2700 cycles a tile.
+// (two chunks of 531 and 586 tokens behind 4200 keys each, 128 heads) against 1830
+// us: 0.45 of the burst matrix rate, 2700 cycles a tile.  The clock is part of that:
+// in a run of calls the power cap holds 1.55 to 1.6 GHz, ten calls after a pause take
+// 1585 us (a selected chunk 1100 and 940).  The times beside the choices below are
+// short runs of graph replays, 1700 us for this case.
 //
 // Work items.  An item is a group of query rows and a part of their keys.  A
 // selection's item is one query; a dense item is up to 128 / heads consecutive
@@ -769,6 +772,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) attn_paged_kernel(const __grid_
                     __syncwarp();
                 }
             }
+            // (__log2f: 2^-22 absolute for l near 1, 2 ulp elsewhere; a score is off by more)
             write_lse(it, item, l != 0.f ? m_used + __log2f(l) : -INFINITY);
             return true;
         };

@@ -4,9 +4,10 @@
 // the e4m3 codes with one fp32 scale per token, amax / 448).
 //
 // One warp per token, its row and key in registers (a warp for each of the two
-// looks the position up twice: 14.6 us against 13.0 for 9400 tokens).  Bound by
-// latency: a decode step moves a few hundred KB; a prefill chunk's warps each wait
-// for the sequence, the page and the row in turn (27 MB in 13 us, a third of HBM).
+// looks the position up twice: graph replays 14.6 us against 13.0 for 9154 tokens).
+// Bound by latency: a decode step moves a few hundred KB; a prefill chunk's warps
+// each wait for the sequence, the page and the row in turn (27 MB in 15 us, 0.28 of
+// the copy bandwidth).
 //
 // The indexer key is computed in 64 bits.  Its codes are a rounding to 4
 // significant bits: an fp32 error of 1e-7 moves about one value in a million

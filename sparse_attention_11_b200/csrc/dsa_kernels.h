@@ -241,7 +241,9 @@ struct RowXform {
     int64_t rope_positions;
 };
 constexpr int kRowMaxDim = 2048;
-constexpr int kNormRopeBwdBlocks = 148 * 2;  // as many as are resident
+// Two blocks an SM: as many as are resident up to 128 and from 257 to 768 columns; of
+// the others one is, and the blocks run in two waves.
+constexpr int kNormRopeBwdBlocks = 148 * 2;
 
 struct NormRopeArgs {
     SeqView sv;

@@ -15,8 +15,9 @@
 // dy once, dx once); a group of 8 lanes (dim <= 256) or 32 lanes holds a row in
 // registers as 16-byte chunks, so the norm's reduction and the rotation need
 // no second read.  All arithmetic is fp32; the result is rounded once.  8192 x 128
-// rows of 576 in bf16: 427 us, 0.87 of the copy bandwidth; the backward of 236K
-// rows of 128 in bf16: 41 us, 0.68 (16 warps an SM at 128 registers).
+// rows of 576 in bf16: 439 us, 0.84 of the copy bandwidth; the backward of 232K
+// rows of 128 in bf16: 43 us, 0.64 (16 warps an SM at 128 registers).  The times
+// beside the choices below are of graph replays (429 and 41.6 us for these two).
 //
 // dw is summed in a fixed order, whatever the launch: each lane sums its
 // columns over its block's rows, the block's groups are added in order, and a
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 4 : 1) norm_rope_kernel(
     RowWalk<2> w = walk_from(r0 + sub, a.heads, st, sh);
     TokenPos tp;
     // One row at a time: many small warps hide the loads better than rows in flight
-    // (a row ahead: 120 registers, 565 us for 8192 x 128 x 576 in bf16).
+    // (a row ahead: 120 registers, 565 us for 8192 x 128 x 576 in bf16 against 427).
     for (int i = sub; i < n + sub; i += RPW) {
         bool live = i < n;
         Raw8<T> cur[NC];
@@ -154,7 +155,9 @@ __global__ void __launch_bounds__(NR_THREADS, NC <= 3 ? 2 : 1) norm_rope_bwd_ker
             if (a.ra.weight && c < n) load_weight8(a.ra.weight, c, wt[i]);
         }
     // The next row is in flight while this one is worked on where that does not
-    // spill (heads of 128 in bf16: 51 -> 41 us; 576 columns in fp32 spill: 14 -> 21).
+    // spill.  In bf16 without and with, us: 232K heads of 128 51, 41; 116K heads of 192
+    // 70, 58 and of 256 72, 62; 29K rows of 1024 70, 60 (one block an SM either way).
+    // 576 columns in fp32 spill: 14, 21.
     constexpr bool AHEAD = sizeof(T) == 2 ? NC <= 2 || NC == 4 : NC == 1;
     Raw8<T> cx[NC], cg[NC];
     auto fetch = [&](bool have) {

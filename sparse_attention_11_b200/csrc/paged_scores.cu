@@ -20,8 +20,9 @@
 // as are resident and each takes an equal stretch of all sequences' key tiles,
 // found by a scan over the lengths.  The queries travel with every tile (128 bytes
 // beside 16 KB for a decode), so a stretch may cross sequences at any tile.  A CTA
-// per 28 tiles of one sequence measured 87 us (64 caches of 16K to 64K keys), this
-// form 66 us: 0.81 of the copy bandwidth.
+// per 28 tiles of one sequence measured 87 us (64 caches of 16K to 64K keys, graph
+// replays, as all times beside choices here), this form 66 us; a call among others
+// takes 70 us, 0.77 of the copy bandwidth.
 #include "rows.cuh"
 
 namespace dsa {
@@ -665,7 +666,10 @@ static bool ps_launch(PagedScoresArgs a, cudaStream_t s) {
     const int64_t units = (a.max_seqlen_q + NQ - 1) / NQ * a.sv.batch;
     if (tiles <= 0 || units <= 0) return true;
     // Key tiles a CTA: as many CTAs as are resident for one sequence (1000 x 32000:
-    // 33 us against 36 with four an SM), twice that for several of different lengths.
+    // 33 us against 36 with four an SM), twice that for several, whose lengths may
+    // differ much: 63 single tokens and a chunk of 17 over 16K to 64K keys 154 us
+    // against 165.  Sequences alike pay for it (queries x keys: 3 x 385 x 20K 42.9
+    // against 40.7, 8 x 128 x 10K 25.5 against 24.4, 32 x 20 x 5K 22.6 against 20.4).
     const int64_t ctas = 148 * (a.sv.batch == 1 ? 2 : 4);
     int64_t per = (tiles * units + ctas - 1) / ctas;
     per = per < 2 ? 2 : per > 64 ? 64 : per;
@@ -681,6 +685,10 @@ static bool ps_launch(PagedScoresArgs a, cudaStream_t s) {
 
 bool launch_paged_scores(const PagedScoresArgs& a, bool e4m3, cudaStream_t s) {
     if (a.row_count <= 0 || a.cols <= 0) return true;
+    // By the longest query count, the only one that the host has.  A sequence of more
+    // than 16 takes the others with it: 63 single tokens and one of 16 over 16K to 64K
+    // keys 108 us, with one of 17 154 us (the same on the kernel for few queries would
+    // read the longer one's keys twice, and 64 times for 1000).
     if (e4m3) return a.max_seqlen_q <= 16 ? pfw_launch(a, s) : ps_launch<128>(a, s);
     const int64_t gx = (a.cols + PSF_KEYS - 1) / PSF_KEYS;
     // rows on the grid's second axis, at most 65535 a launch

@@ -105,8 +105,8 @@ DSA_DEV float group_sum(float x) {
 }
 
 // A row's reciprocal root mean square, from mean square + eps.  rsqrtf is within 2
-// ulp; 1 / sqrtf measured 43.6 us against 41.6 (backward of 232K heads of 128 in
-// bf16) and 33.8 against 33.1 (forward).  Every path takes this one, so that a row's
+// ulp; 1 / sqrtf measured 43.6 us against 41.6 (graph replays, backward of 232K heads
+// of 128 in bf16) and 33.8 against 33.1 (forward).  Every path takes this one, so that a row's
 // alignment does not change it.
 DSA_DEV float row_rstd(float ms) { return rsqrtf(ms); }
 
